@@ -10,13 +10,18 @@ ctypes with the same names:
   (Sec. 3.3, Eq. 13); ``dynrad_attn_backward`` is its gradient under the
   same mask.
 
+For sequences that grow piece by piece, a paged K / V cache (bf16, or 8 bits
+with power-of-two scales): ``KVCache``, ``dynrad_cache_write``,
+``dynrad_cache_read`` and ``dynrad_cache_attn``.
+
 ``workloads`` holds the seeded synthetic inputs.  The binding is imported
 lazily so that the workload generator can be used without a GPU.
 """
 
 _ABI_NAMES = ("dynrad_num_blocks", "dynrad_build_candidates", "dynrad_build_candidates_into", "dynrad_select_blocks",
               "dynrad_sparse_attn", "dynrad_attn_backward", "dynrad_device_status", "dynrad_select_workspace_bytes",
-              "SelectBuffers", "DynradError", "make_geom", "lib")
+              "SelectBuffers", "DynradError", "make_geom", "lib",
+              "KVCache", "dynrad_cache_write", "dynrad_cache_read", "dynrad_cache_attn")
 
 
 def __getattr__(name):

@@ -50,7 +50,14 @@ EXPORTED = (
     "dynrad_attn_backward_workspace_bytes",
     "dynrad_attn_backward",
     "dynrad_debug_attn_stall",
+    "dynrad_cache_write",
+    "dynrad_cache_read",
+    "dynrad_cache_attn_workspace_bytes",
+    "dynrad_cache_attn",
 )
+
+CACHE_FORMATS = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, torch.int8: 2}
+CACHE_GROUP = 32   # channels under one scale of the 8-bit formats
 
 
 class DynradGeom(ctypes.Structure):
@@ -81,6 +88,32 @@ class DynradHostRun(ctypes.Structure):
         ("rho_or_tau", ctypes.c_double),
         ("o_host", ctypes.c_void_p),
         ("lse_host", ctypes.c_void_p),
+    ]
+
+
+class DynradKvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+    ]
+
+
+class DynradSeqs(ctypes.Structure):
+    _fields_ = [
+        ("page_table", ctypes.c_void_p),
+        ("cu_seq", ctypes.c_void_p),
+        ("kv_len", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("num_tokens", ctypes.c_int32),
     ]
 
 
@@ -163,6 +196,16 @@ def lib() -> ctypes.CDLL:
                                            _I64, ctypes.c_float, _VP, _VP, _VP, _VP, _SZ, _VP]
         L.dynrad_debug_attn_stall.restype = ctypes.c_int
         L.dynrad_debug_attn_stall.argtypes = [ctypes.c_uint64, _I32]
+        CP, SP = ctypes.POINTER(DynradKvCache), ctypes.POINTER(DynradSeqs)
+        L.dynrad_cache_write.restype = ctypes.c_int
+        L.dynrad_cache_write.argtypes = [CP, SP, _VP, _I64, _I64, _VP, _I64, _I64, _VP]
+        L.dynrad_cache_read.restype = ctypes.c_int
+        L.dynrad_cache_read.argtypes = [CP, SP, _VP, _I64, _I64, _VP, _I64, _I64, _VP]
+        L.dynrad_cache_attn_workspace_bytes.restype = _SZ
+        L.dynrad_cache_attn_workspace_bytes.argtypes = [CP, _I32, _I32, _I32]
+        L.dynrad_cache_attn.restype = ctypes.c_int
+        L.dynrad_cache_attn.argtypes = [CP, SP, _VP, _I64, _I64, _I32, _I32, _I32, ctypes.c_float, _VP, _I64, _I64,
+                                        _VP, _VP, _SZ, _VP]
         _lib = L
     return _lib
 
@@ -496,3 +539,162 @@ def dynrad_debug_attn_stall(wait_ns: int = 0, stall_step: int = -1) -> None:
     pipeline waits and the step at which its MMA warp waits for a barrier
     nothing completes; (0, -1) restores normal operation.  Process-wide."""
     _check(lib().dynrad_debug_attn_stall(int(wait_ns), int(stall_step)), "dynrad_debug_attn_stall")
+
+
+# ---------------------------------------------------------------- paged cache --
+class KVCache:
+    """The pages of a K / V cache (caller-owned tensors).
+
+    k, v: [num_pages, heads, page, dim] contiguous, bf16, float8_e4m3fn or int8
+    (page 16, 32, 64 or 128; dim 64 or 128); k_scale, v_scale: uint8
+    [num_pages, heads, page, dim / 32] exponent bytes of the 8-bit formats, None
+    for bf16.  ``KVCache.empty`` makes them (uninitialised: what was never
+    written is never looked at)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.dtype not in CACHE_FORMATS or v.dtype != k.dtype or v.shape != k.shape:
+            raise ValueError("k and v must be [num_pages, heads, page, dim] tensors of one shape, bf16, float8_e4m3fn "
+                             "or int8")
+        if not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("the pages must be contiguous")
+        pages, heads, page, dim = k.shape
+        fmt = CACHE_FORMATS[k.dtype]
+        if fmt:
+            want = (pages, heads, page, dim // CACHE_GROUP)
+            for t in (k_scale, v_scale):
+                if t is None or t.dtype != torch.uint8 or t.shape != want or not t.is_contiguous():
+                    raise ValueError(f"an 8-bit cache needs contiguous uint8 k_scale and v_scale of shape {want}")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no scales")
+        for t in (v, k_scale, v_scale):
+            if t is not None and t.device != k.device:
+                raise ValueError("the cache's tensors must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.heads, self.page, self.dim, self.device = heads, page, dim, k.device
+        self.c = DynradKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fmt else None,
+                               v_scale.data_ptr() if fmt else None, pages, heads, page, dim, fmt)
+
+    @classmethod
+    def empty(cls, num_pages, heads, page, dim, dtype=torch.bfloat16, device=None):
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        k, v = (torch.empty((num_pages, heads, page, dim), dtype=dtype, device=device) for _ in range(2))
+        ks, vs = (None if dtype == torch.bfloat16 else
+                  torch.empty((num_pages, heads, page, dim // CACHE_GROUP), dtype=torch.uint8, device=device)
+                  for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+def _cache_seqs(cache, page_table, cu_seq, kv_len, num_tokens) -> DynradSeqs:
+    """The C struct of a call's sequences, after host checks that keep the
+    kernels inside the tensors.  Raises ValueError."""
+    if page_table.dim() != 2 or cu_seq.dim() != 1 or kv_len.dim() != 1:
+        raise ValueError("page_table is [S, max_pages], cu_seq [S + 1], kv_len [S]")
+    S, cols = page_table.shape
+    if page_table.dtype != torch.int32 or cu_seq.dtype != torch.int32 or kv_len.dtype != torch.int32:
+        raise ValueError("page_table, cu_seq and kv_len must be int32 tensors")
+    if cu_seq.shape[0] != S + 1 or kv_len.shape[0] != S:
+        raise ValueError(f"page_table has {S} rows: cu_seq needs {S + 1} entries and kv_len {S}")
+    if not (cu_seq.is_contiguous() and kv_len.is_contiguous()) or (cols > 1 and page_table.stride(1) != 1):
+        raise ValueError("cu_seq and kv_len must be contiguous, page_table in its rows")
+    if page_table.device != cache.device or cu_seq.device != cache.device or kv_len.device != cache.device:
+        raise ValueError("page_table, cu_seq and kv_len must be on the cache's device")
+    stride = page_table.stride(0) if S > 1 else cols
+    if stride < cols:
+        raise ValueError("page_table's rows must not overlap")
+    return DynradSeqs(page_table.data_ptr(), cu_seq.data_ptr(), kv_len.data_ptr(), stride, S, cols, num_tokens)
+
+
+def _cache_rows(cache, name, t, heads, tokens=None, head_major=False, written=False):
+    """(token stride, head stride) of a bf16 [T, heads, D] tensor ([heads, T, D]
+    with head_major) whose rows the kernels move 16 bytes at a time."""
+    ti, hi = (1, 0) if head_major else (0, 1)
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.shape[2] != cache.dim or t.shape[hi] != heads or (
+            tokens is not None and t.shape[ti] != tokens):
+        raise ValueError(f"{name} must be bf16 [{'heads, T' if head_major else 'T, heads'}, {cache.dim}] with "
+                         f"{heads} heads" + ("" if tokens is None else f" and {tokens} tokens"))
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on the cache's device")
+    ts = t.stride(ti) if t.shape[ti] > 1 else heads * cache.dim
+    hs = t.stride(hi) if heads > 1 else cache.dim
+    if t.stride(2) != 1 or ts % 8 or hs % 8 or ts < 0 or hs < 0:
+        raise ValueError(f"{name}: the last dimension must be contiguous and the strides multiples of 8 elements")
+    if written and t.numel():
+        a, b = sorted(((ts, t.shape[ti]), (hs, heads)))
+        if (a[1] > 1 and a[0] < cache.dim) or (b[1] > 1 and b[0] < a[0] * (a[1] - 1) + cache.dim):
+            raise ValueError(f"{name} is written: its rows must not overlap")
+    return ts, hs
+
+
+def _require_current(cache):
+    if cache.device.type != "cuda" or cache.device.index != torch.cuda.current_device():
+        raise ValueError("the cache must be on the current CUDA device")
+
+
+def dynrad_cache_write(cache, k, v, page_table, cu_seq, kv_len, stream=None) -> None:
+    """Writes K and V (bf16 [T, heads, D], any strides that are multiples of 8)
+    into the cache: token i of the n that cu_seq gives sequence s goes to its
+    position kv_len[s] - n + i (kv_len counts the new tokens)."""
+    T = k.shape[0]
+    sq = _cache_seqs(cache, page_table, cu_seq, kv_len, T)
+    kt, kh = _cache_rows(cache, "k", k, cache.heads)
+    vt, vh = _cache_rows(cache, "v", v, cache.heads, T)
+    _require_current(cache)
+    _check(lib().dynrad_cache_write(ctypes.byref(cache.c), ctypes.byref(sq), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                                    _stream(stream)), "dynrad_cache_write")
+
+
+def dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens=None, head_major=False, out=None, stream=None):
+    """(K, V) that the cache holds at the tokens' positions, bf16 [T, heads, D]
+    or, head_major, [heads, T, D] (with one sequence the tensors that
+    dynrad_select_blocks and dynrad_sparse_attn take, but for the batch axis).
+    T = num_tokens, or that of the tensors in ``out``; rows behind
+    cu_seq[-1] are left as they are."""
+    if out is None:
+        if num_tokens is None:
+            raise ValueError("num_tokens or out is needed")
+        shape = (cache.heads, num_tokens) if head_major else (num_tokens, cache.heads)
+        out = tuple(torch.empty(shape + (cache.dim,), dtype=torch.bfloat16, device=cache.device) for _ in range(2))
+    k, v = out
+    T = k.shape[1 if head_major else 0]
+    if num_tokens is not None and num_tokens != T:
+        raise ValueError(f"out holds {T} tokens, not {num_tokens}")
+    sq = _cache_seqs(cache, page_table, cu_seq, kv_len, T)
+    kt, kh = _cache_rows(cache, "out", k, cache.heads, T, head_major, written=True)
+    vt, vh = _cache_rows(cache, "out", v, cache.heads, T, head_major, written=True)
+    _require_current(cache)
+    _check(lib().dynrad_cache_read(ctypes.byref(cache.c), ctypes.byref(sq), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                                   _stream(stream)), "dynrad_cache_read")
+    return k, v
+
+
+def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, scale=0.0, out=None, lse=None,
+                      workspace=None, stream=None):
+    """Attention of the new tokens q (bf16 [T, heads, D], heads a multiple of the
+    cache's) over what the cache holds, their own keys among it.  frame = 0: a
+    token sees its whole sequence; frame >= 1: up to the end of its own frame of
+    that many positions (1: token-causal); window >= 1: of those the last
+    ``window`` frames.  Returns (o bf16 [T, heads, D], lse fp32 [heads, T]); rows
+    behind cu_seq[-1] are left as they are."""
+    if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache.heads:
+        raise ValueError("q must be [T, heads, D] with a multiple of the cache's heads")
+    T, H, D = q.shape
+    sq = _cache_seqs(cache, page_table, cu_seq, kv_len, T)
+    qt, qh = _cache_rows(cache, "q", q, H)
+    if (T > 1 and qt == 0) or (H > 1 and qh == 0):
+        raise ValueError("q must not be expanded")
+    o = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+    ot, oh = _cache_rows(cache, "out", o, H, T, written=True)
+    lse_t = torch.empty((H, T), dtype=torch.float32, device=q.device) if lse is None else lse
+    if lse_t.dtype != torch.float32 or lse_t.shape != (H, T) or not lse_t.is_contiguous() or lse_t.device != q.device:
+        raise ValueError("lse must be a contiguous fp32 [heads, T] tensor")
+    _require_current(cache)
+    L = lib()
+    if workspace is None:
+        need = L.dynrad_cache_attn_workspace_bytes(ctypes.byref(cache.c), sq.num_seqs, T, H)
+        if need == 0:
+            raise DynradError(DYNRAD_ERR_INVALID_ARG, "dynrad_cache_attn_workspace_bytes")
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(L.dynrad_cache_attn(ctypes.byref(cache.c), ctypes.byref(sq), q.data_ptr(), qt, qh, H, int(frame),
+                               int(window), float(scale), o.data_ptr(), ot, oh, lse_t.data_ptr(),
+                               workspace.data_ptr(), workspace.numel(), _stream(stream)), "dynrad_cache_attn")
+    return o, lse_t

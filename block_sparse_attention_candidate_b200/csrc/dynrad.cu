@@ -15,11 +15,13 @@
 #include <vector>
 
 #include "attention.cuh"
+#include "cacheattn.cuh"
 #include "candidates.cuh"
 #include "common.cuh"
 #include "backward.cuh"
 #include "optin.h"
 #include "dyntok.cuh"
+#include "kvcache.cuh"
 #include "sampling.cuh"
 #include "select.cuh"
 
@@ -1100,4 +1102,168 @@ extern "C" int dynrad_select_blocks_static_scratch(
   return dynrad_select_blocks(q, k, B, H, N, D, geom, cand_row_ptr, cand_col, cand_nnz, cand_max_row, forced_lo,
                               forced_hi, mode, rho_or_tau, row_ptr, col_idx, col_cap, scores_out, scratch, need,
                               stream);
+}
+
+// ---------------------------------------------------------------------------
+// Paged K / V cache
+// ---------------------------------------------------------------------------
+namespace {
+
+// Checks of the two structs that all three cache calls share.
+int check_cache(const dynrad_kv_cache* c, const dynrad_seqs* s, CacheDev* cd, SeqsDev* sd) {
+  if (c == nullptr || s == nullptr || c->k == nullptr || c->v == nullptr) return DYNRAD_ERR_INVALID_ARG;
+  if (c->format < DYNRAD_CACHE_BF16 || c->format > DYNRAD_CACHE_INT8) return DYNRAD_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->heads < 1) return DYNRAD_ERR_INVALID_ARG;
+  if (c->dim != 64 && c->dim != 128) return DYNRAD_ERR_UNSUPPORTED;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return DYNRAD_ERR_UNSUPPORTED;
+  if (c->num_pages > INT32_MAX || c->num_pages * c->heads > INT32_MAX / c->page) return DYNRAD_ERR_UNSUPPORTED;
+  if (!aligned16(c->k) || !aligned16(c->v)) return DYNRAD_ERR_INVALID_ARG;
+  if (c->format != DYNRAD_CACHE_BF16 &&
+      (c->k_scale == nullptr || c->v_scale == nullptr || !aligned16(c->k_scale) || !aligned16(c->v_scale)))
+    return DYNRAD_ERR_INVALID_ARG;
+  if (s->num_seqs < 0 || s->num_tokens < 0 || s->max_pages < 0 || s->table_stride < s->max_pages)
+    return DYNRAD_ERR_INVALID_ARG;
+  if (s->max_pages > INT32_MAX / c->page) return DYNRAD_ERR_UNSUPPORTED;
+  if (s->num_seqs > 0 && (s->page_table == nullptr || s->cu_seq == nullptr || s->kv_len == nullptr))
+    return DYNRAD_ERR_INVALID_ARG;
+  cd->k = static_cast<uint8_t*>(c->k);
+  cd->v = static_cast<uint8_t*>(c->v);
+  cd->k_scale = c->k_scale;
+  cd->v_scale = c->v_scale;
+  cd->num_pages = c->num_pages;
+  cd->heads = c->heads;
+  cd->page_shift = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
+  sd->page_table = s->page_table;
+  sd->cu_seq = s->cu_seq;
+  sd->kv_len = s->kv_len;
+  sd->table_stride = s->table_stride;
+  sd->num_seqs = s->num_seqs;
+  sd->max_pages = s->max_pages;
+  sd->num_tokens = s->num_tokens;
+  return DYNRAD_OK;
+}
+
+// A strided bf16 [tokens, heads, D] operand of 16-byte rows.
+bool bad_rows(const void* p, int64_t token_stride, int64_t head_stride) {
+  return p == nullptr || !aligned16(p) || token_stride < 0 || head_stride < 0 || (token_stride & 7) != 0 ||
+         (head_stride & 7) != 0;
+}
+
+int cache_move_grid(const SeqsDev& s, unsigned* grid) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DYNRAD_ERR_CUDA;
+  const int64_t chunks = (static_cast<int64_t>(s.num_tokens) + kCacheTokens - 1) / kCacheTokens;
+  *grid = static_cast<unsigned>(std::min<int64_t>(chunks, static_cast<int64_t>(sms) * 8));
+  return DYNRAD_OK;
+}
+
+}  // namespace
+
+// f is instantiated for the cache's head dim and format
+#define DYNRAD_CACHE_DISPATCH(dim, fmt, f)                                                      \
+  do {                                                                                          \
+    if ((dim) == 128) {                                                                         \
+      if ((fmt) == DYNRAD_CACHE_BF16) f(128, kCacheBf16);                                       \
+      else if ((fmt) == DYNRAD_CACHE_E4M3) f(128, kCacheE4m3);                                  \
+      else f(128, kCacheInt8);                                                                  \
+    } else {                                                                                    \
+      if ((fmt) == DYNRAD_CACHE_BF16) f(64, kCacheBf16);                                        \
+      else if ((fmt) == DYNRAD_CACHE_E4M3) f(64, kCacheE4m3);                                   \
+      else f(64, kCacheInt8);                                                                   \
+    }                                                                                           \
+  } while (0)
+
+extern "C" int dynrad_cache_write(const dynrad_kv_cache* cache, const dynrad_seqs* seqs, const void* k,
+                                  int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                                  int64_t v_token_stride, int64_t v_head_stride, dynrad_stream_t stream) {
+  CacheWriteParams p;
+  int rc = check_cache(cache, seqs, &p.c, &p.s);
+  if (rc != DYNRAD_OK) return rc;
+  if (p.s.num_seqs == 0 || p.s.num_tokens == 0) return DYNRAD_OK;
+  if (bad_rows(k, k_token_stride, k_head_stride) || bad_rows(v, v_token_stride, v_head_stride))
+    return DYNRAD_ERR_INVALID_ARG;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_token = k_token_stride;
+  p.k_head = k_head_stride;
+  p.v_token = v_token_stride;
+  p.v_head = v_head_stride;
+  unsigned grid = 0;
+  if ((rc = cache_move_grid(p.s, &grid)) != DYNRAD_OK) return rc;
+#define DYNRAD_CACHE_F(D_, F_) cache_write_kernel<D_, F_><<<grid, kCacheThreads, 0, as_stream(stream)>>>(p)
+  DYNRAD_CACHE_DISPATCH(cache->dim, cache->format, DYNRAD_CACHE_F);
+#undef DYNRAD_CACHE_F
+  return launch_status();
+}
+
+extern "C" int dynrad_cache_read(const dynrad_kv_cache* cache, const dynrad_seqs* seqs, void* k,
+                                 int64_t k_token_stride, int64_t k_head_stride, void* v, int64_t v_token_stride,
+                                 int64_t v_head_stride, dynrad_stream_t stream) {
+  CacheReadParams p;
+  int rc = check_cache(cache, seqs, &p.c, &p.s);
+  if (rc != DYNRAD_OK) return rc;
+  if (p.s.num_seqs == 0 || p.s.num_tokens == 0) return DYNRAD_OK;
+  if (bad_rows(k, k_token_stride, k_head_stride) || bad_rows(v, v_token_stride, v_head_stride))
+    return DYNRAD_ERR_INVALID_ARG;
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  p.k_token = k_token_stride;
+  p.k_head = k_head_stride;
+  p.v_token = v_token_stride;
+  p.v_head = v_head_stride;
+  unsigned grid = 0;
+  if ((rc = cache_move_grid(p.s, &grid)) != DYNRAD_OK) return rc;
+#define DYNRAD_CACHE_F(D_, F_) cache_read_kernel<D_, F_><<<grid, kCacheThreads, 0, as_stream(stream)>>>(p)
+  DYNRAD_CACHE_DISPATCH(cache->dim, cache->format, DYNRAD_CACHE_F);
+#undef DYNRAD_CACHE_F
+  return launch_status();
+}
+
+extern "C" size_t dynrad_cache_attn_workspace_bytes(const dynrad_kv_cache* cache, int32_t num_seqs,
+                                                    int32_t num_tokens, int32_t heads) {
+  if (cache == nullptr || num_seqs < 0 || num_tokens < 0 || heads < 1 || cache->heads < 1 ||
+      heads % cache->heads != 0 || (cache->dim != 64 && cache->dim != 128))
+    return 0;
+  return 256;
+}
+
+extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs* seqs, const void* q,
+                                 int64_t q_token_stride, int64_t q_head_stride, int32_t heads, int32_t frame,
+                                 int32_t window, float scale, void* o, int64_t o_token_stride, int64_t o_head_stride,
+                                 float* lse, void* workspace, size_t workspace_bytes, dynrad_stream_t stream) {
+  CacheAttnParams p;
+  int rc = check_cache(cache, seqs, &p.c, &p.s);
+  if (rc != DYNRAD_OK) return rc;
+  if (heads < 1 || heads % cache->heads != 0 || frame < 0 || window < 0 || (frame == 0 && window > 0))
+    return DYNRAD_ERR_INVALID_ARG;
+  if (!(scale >= 0.0f) || !std::isfinite(scale)) return DYNRAD_ERR_INVALID_ARG;
+  if (heads / cache->heads > 128) return DYNRAD_ERR_UNSUPPORTED;
+  if (p.s.num_seqs == 0 || p.s.num_tokens == 0) return DYNRAD_OK;
+  if (bad_rows(q, q_token_stride, q_head_stride) || bad_rows(o, o_token_stride, o_head_stride) || lse == nullptr ||
+      workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return DYNRAD_ERR_INVALID_ARG;
+  if (workspace_bytes < dynrad_cache_attn_workspace_bytes(cache, seqs->num_seqs, seqs->num_tokens, heads))
+    return DYNRAD_ERR_CAPACITY;
+  const float sc = scale == 0.0f ? 1.0f / std::sqrt(static_cast<float>(cache->dim)) : scale;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.q_token = q_token_stride;
+  p.q_head = q_head_stride;
+  p.o_token = o_token_stride;
+  p.o_head = o_head_stride;
+  p.heads = heads;
+  p.group = heads / cache->heads;
+  p.frame = frame;
+  p.window = window;
+  p.scale_log2 = sc * 1.4426950408889634f;
+  const int64_t rows = static_cast<int64_t>(seqs->num_tokens) * heads;
+  if ((rows + 3) / 4 > INT32_MAX) return DYNRAD_ERR_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+#define DYNRAD_CACHE_F(D_, F_) cache_attn_kernel<D_, F_><<<grid, 128, 0, as_stream(stream)>>>(p)
+  DYNRAD_CACHE_DISPATCH(cache->dim, cache->format, DYNRAD_CACHE_F);
+#undef DYNRAD_CACHE_F
+  return launch_status();
 }

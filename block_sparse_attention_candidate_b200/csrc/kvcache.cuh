@@ -1,0 +1,335 @@
+// Paged K / V cache: where a token stands, and the kernels that write new
+// tokens into the pages and read them back.
+//
+// Layout.  A page holds `page` tokens of every K / V head, head-major
+// ([num_pages][heads][page][D]), so the tokens of one head of one page are one
+// contiguous tile: the unit the attention kernel loads.  Formats: bf16, or 8
+// bits a channel (e4m3 / int8) with one scale for every 32 channels of a token,
+// kept as the biased exponent byte of a power of two
+// ([num_pages][heads][page][D / 32]).  A power of two makes what is stored an
+// exact bf16 number (4 or 8 significant bits), so reading back and the
+// attention's operands round nothing: the one rounding is the write's.
+//
+// Quantisation of 32 channels x with a = max |x|:  s = 2^e with the least e
+// such that a <= c_max s (c_max = 448 for e4m3, 127 for int8), e >= -117 (then
+// the smallest e4m3 step 2^-9 s is still a normal bf16 number); code =
+// round-to-nearest-even(x / s); magnitudes over 240 * 2^120 (e4m3) or 127 * 2^121
+// (int8), whose code would stand for 2^128, are stored as those.  An infinity or NaN among the 32 gives the
+// exponent byte 255, and all 32 read back as NaN.
+//
+// Both kernels are one pass over the data and bound by HBM: per (token, head)
+// they move 2 * D * 2 bytes of bf16 and 2 * (D + D / 32) of the 8-bit pages
+// (2 * D * 2 again for bf16 pages).
+#pragma once
+
+#include "common.cuh"
+
+namespace dynrad {
+
+constexpr int kCacheBf16 = 0, kCacheE4m3 = 1, kCacheInt8 = 2;
+constexpr int kCacheGroup = 32;          // channels under one scale
+constexpr int kCacheLeastExp = -117;     // least exponent of a scale
+constexpr uint32_t kCacheNanScale = 255;
+
+struct CacheDev {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int64_t num_pages;
+  int32_t heads;
+  int32_t page_shift;   // log2(tokens a page)
+};
+
+struct SeqsDev {
+  const int32_t* page_table;
+  const int32_t* cu_seq;
+  const int32_t* kv_len;
+  int64_t table_stride;
+  int32_t num_seqs;
+  int32_t max_pages;
+  int32_t num_tokens;
+};
+
+// Tokens [begin, end) and cached length of a sequence, held inside the caller's
+// arrays whatever the device arrays say (a bad value is recorded).
+struct SeqSpan {
+  int32_t begin, end, len;
+};
+
+__device__ __forceinline__ SeqSpan seq_span(const SeqsDev& s, int i, int page_shift) {
+  SeqSpan r;
+  const int32_t a = s.cu_seq[i], b = s.cu_seq[i + 1], n = s.kv_len[i];
+  r.begin = min(max(a, 0), s.num_tokens);
+  r.end = min(max(b, r.begin), s.num_tokens);
+  const int64_t cap = static_cast<int64_t>(s.max_pages) << page_shift;
+  r.len = static_cast<int32_t>(min(static_cast<int64_t>(max(n, 0)), cap));
+  if (r.begin != a || r.end != b || r.len != n) record_error(DYNRAD_ERR_DEVICE);
+  return r;
+}
+
+// The sequence that token t belongs to, -1 if none (t lies behind the last one).
+__device__ __forceinline__ int seq_of_token(const SeqsDev& s, int t) {
+  int lo = 0, hi = s.num_seqs;   // last i with cu_seq[i] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.cu_seq[mid] <= t) lo = mid; else hi = mid;
+  }
+  return s.cu_seq[lo] <= t && t < s.cu_seq[lo + 1] ? lo : -1;
+}
+
+// Row (page * heads) << page_shift | slot of a cached position; a page outside the
+// pool is recorded and gives -1.  A row's head h is page tokens further on.
+__device__ __forceinline__ int64_t cache_row(const CacheDev& c, const SeqsDev& s, int seq, int32_t pos) {
+  const int32_t pg = s.page_table[static_cast<int64_t>(seq) * s.table_stride + (pos >> c.page_shift)];
+  if (pg < 0 || pg >= c.num_pages) {
+    record_error(DYNRAD_ERR_DEVICE);
+    return -1;
+  }
+  return ((static_cast<int64_t>(pg) * c.heads) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 2^e as a bf16 pair, -127 <= e <= 127 (2^-127 is a subnormal)
+__device__ __forceinline__ uint32_t pow2_bf16x2(int e) {
+  const uint32_t b = e < -126 ? 0x40u : static_cast<uint32_t>(e + 127) << 7;
+  return b | (b << 16);
+}
+
+// Four stored bytes -> four bf16 numbers, before their scale.  e4m3: the seven
+// low bits moved to bf16's exponent and mantissa are the value times 2^-120
+// (subnormals included).  int8: 128 + the seven low bits is a bf16 number, and
+// so is the 128 or 256 to take from it.
+template <int FMT>
+__device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == kCacheE4m3) {
+    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);   // byte in the high half
+    lo = (a & 0x80008000u) | ((a & 0x7f007f00u) >> 4);
+    hi = (b & 0x80008000u) | ((b & 0x7f007f00u) >> 4);
+  } else {
+    const uint32_t a = __byte_perm(w, 0x43434343u, 0x4140), b = __byte_perm(w, 0x43434343u, 0x4342);
+    lo = sub_bf16x2(a & 0xff7fff7fu, a & 0xff80ff80u);
+    hi = sub_bf16x2(b & 0xff7fff7fu, b & 0xff80ff80u);
+  }
+}
+
+// Factors of a scale byte for what unpack4 gives: the second is 1 unless the
+// first would leave bf16's range (scales over 2^7 of e4m3 pages).
+template <int FMT>
+__device__ __forceinline__ void scale_factors(uint32_t byte, uint32_t& f1, uint32_t& f2) {
+  f2 = 0x3f803f80u;
+  if (byte == kCacheNanScale) {
+    f1 = 0x7fc07fc0u;
+    return;
+  }
+  int e = static_cast<int>(byte) - 127 + (FMT == kCacheE4m3 ? 120 : 0);
+  if (e > 127) {
+    f2 = pow2_bf16x2(e - 127);
+    e = 127;
+  }
+  f1 = pow2_bf16x2(e);
+}
+
+// 16 stored bytes under one scale -> 16 bf16 numbers.
+template <int FMT>
+__device__ __forceinline__ void dequant16(const uint4& w, uint32_t byte, uint4& o0, uint4& o1) {
+  uint32_t f1, f2;
+  scale_factors<FMT>(byte, f1, f2);
+  unpack4<FMT>(w.x, o0.x, o0.y);
+  unpack4<FMT>(w.y, o0.z, o0.w);
+  unpack4<FMT>(w.z, o1.x, o1.y);
+  unpack4<FMT>(w.w, o1.z, o1.w);
+  o0.x = mul_bf16x2(o0.x, f1); o0.y = mul_bf16x2(o0.y, f1); o0.z = mul_bf16x2(o0.z, f1); o0.w = mul_bf16x2(o0.w, f1);
+  o1.x = mul_bf16x2(o1.x, f1); o1.y = mul_bf16x2(o1.y, f1); o1.z = mul_bf16x2(o1.z, f1); o1.w = mul_bf16x2(o1.w, f1);
+  if (FMT == kCacheE4m3 && f2 != 0x3f803f80u) {
+    o0.x = mul_bf16x2(o0.x, f2); o0.y = mul_bf16x2(o0.y, f2); o0.z = mul_bf16x2(o0.z, f2); o0.w = mul_bf16x2(o0.w, f2);
+    o1.x = mul_bf16x2(o1.x, f2); o1.y = mul_bf16x2(o1.y, f2); o1.z = mul_bf16x2(o1.z, f2); o1.w = mul_bf16x2(o1.w, f2);
+  }
+}
+
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four bf16 numbers (two pairs), already divided by their scale -> four codes.
+template <int FMT>
+__device__ __forceinline__ uint32_t pack4(uint32_t p0, uint32_t p1) {
+  const float a = __uint_as_float(p0 << 16), b = __uint_as_float(p0 & 0xffff0000u);
+  const float c = __uint_as_float(p1 << 16), d = __uint_as_float(p1 & 0xffff0000u);
+  if (FMT == kCacheE4m3) return cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16);
+  const uint32_t i0 = __float2int_rn(a), i1 = __float2int_rn(b), i2 = __float2int_rn(c), i3 = __float2int_rn(d);
+  return __byte_perm(__byte_perm(i0, i1, 0x0040), __byte_perm(i2, i3, 0x0040), 0x5410);
+}
+
+// Exponent of the scale for 32 channels whose largest |x| has the bf16 bits `a`
+// (finite).  448 = 1.75 * 2^8 and 127 = (1 + 126 / 128) * 2^6, so the mantissa
+// field decides between two exponents.
+template <int FMT>
+__device__ __forceinline__ int scale_exponent(uint32_t a) {
+  const int ex = static_cast<int>(a >> 7) - 127;   // subnormals give -127: below the least exponent either way
+  const uint32_t man = a & 127u;
+  const int e = FMT == kCacheE4m3 ? ex - 8 + (man > 96u ? 1 : 0) : ex - 6 + (man > 126u ? 1 : 0);
+  return max(e, kCacheLeastExp);
+}
+
+constexpr int kCacheThreads = 256;
+constexpr int kCacheTokens = 8;   // tokens a CTA takes at a time
+
+struct CacheWriteParams {
+  CacheDev c;
+  SeqsDev s;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t k_token, k_head, v_token, v_head;   // strides in elements
+};
+
+struct CacheReadParams {
+  CacheDev c;
+  SeqsDev s;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  int64_t k_token, k_head, v_token, v_head;
+};
+
+constexpr int64_t kRowNone = -1;     // nothing to do for this token
+constexpr int64_t kRowZero = -2;     // read back as zeros
+
+// Cache rows of kCacheTokens tokens from t0 on, by the CTA's first threads.
+__device__ __forceinline__ void place_tokens(const CacheDev& c, const SeqsDev& s, int t0, int64_t* rows) {
+  if (threadIdx.x < kCacheTokens) {
+    const int t = t0 + threadIdx.x;
+    int64_t row = kRowNone;
+    if (t < s.num_tokens) {
+      const int seq = seq_of_token(s, t);
+      if (seq >= 0) {
+        const SeqSpan sp = seq_span(s, seq, c.page_shift);
+        const int32_t pos = sp.len - (sp.end - t);
+        row = pos < 0 || t >= sp.end ? kRowZero : cache_row(c, s, seq, pos);
+        if (row < 0) row = kRowZero;
+      }
+    }
+    rows[threadIdx.x] = row;
+  }
+}
+
+// One thread quantises (or copies) 16 channels of K or V of one (token, head):
+// two 16-byte loads, one 16-byte store (two for bf16), its neighbour shares the
+// scale.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheWriteParams p) {
+  constexpr int C = D / 16;   // threads a row
+  __shared__ int64_t rows[kCacheTokens];
+  const int per_token = p.c.heads * 2 * C;
+  for (int t0 = blockIdx.x * kCacheTokens; t0 < p.s.num_tokens; t0 += gridDim.x * kCacheTokens) {
+    __syncthreads();
+    place_tokens(p.c, p.s, t0, rows);
+    __syncthreads();
+    const int units = min(kCacheTokens, p.s.num_tokens - t0) * per_token;
+    for (int u = threadIdx.x; u < ((units + 31) & ~31); u += kCacheThreads) {
+      const int tk = min(u, units - 1) / per_token;
+      const int r = min(u, units - 1) - tk * per_token;
+      const int c = r % C, kv = (r / C) / p.c.heads, h = (r / C) - kv * p.c.heads;
+      const int64_t row = u < units ? rows[tk] : kRowNone;
+      const bool live = row >= 0;
+      uint32_t x[8] = {};
+      if (live) {
+        const __nv_bfloat16* src = kv == 0 ? p.k + (t0 + tk) * p.k_token + h * p.k_head
+                                           : p.v + (t0 + tk) * p.v_token + h * p.v_head;
+        const uint4 a = *reinterpret_cast<const uint4*>(src + c * 16);
+        const uint4 b = *reinterpret_cast<const uint4*>(src + c * 16 + 8);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+      }
+      const int64_t at = row + (static_cast<int64_t>(h) << p.c.page_shift);
+      uint8_t* base = kv == 0 ? p.c.k : p.c.v;
+      if (FMT == kCacheBf16) {
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(base + at * (D * 2) + c * 32);
+          dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+          dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        }
+      } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, x[i] & 0x7fff7fffu);
+        uint32_t a = max(m & 0xffffu, m >> 16);
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        const bool nan = a >= 0x7f80u;
+        // magnitudes that would round to 2^128, past bf16, are held at the largest that does not
+        constexpr uint32_t kMost = FMT == kCacheE4m3 ? 0x7f707f70u : 0x7f7e7f7eu;   // 240 * 2^120, 127 * 2^121
+        if (!nan && a > (kMost & 0xffffu)) {
+          a = kMost & 0xffffu;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __vminu2(x[i] & 0x7fff7fffu, kMost) | (x[i] & 0x80008000u);
+        }
+        const int e = nan ? 0 : scale_exponent<FMT>(a);
+        const uint32_t f = pow2_bf16x2(-e);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t y0 = mul_bf16x2(x[2 * i], f), y1 = mul_bf16x2(x[2 * i + 1], f);
+          w[i] = nan ? 0u : pack4<FMT>(y0, y1);
+        }
+        if (live) {
+          *reinterpret_cast<uint4*>(base + at * D + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          if ((c & 1) == 0) {
+            uint8_t* sc = kv == 0 ? p.c.k_scale : p.c.v_scale;
+            sc[at * (D / kCacheGroup) + (c >> 1)] = nan ? kCacheNanScale : static_cast<uint8_t>(e + 127);
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheReadParams p) {
+  constexpr int C = D / 16;
+  __shared__ int64_t rows[kCacheTokens];
+  const int per_token = p.c.heads * 2 * C;
+  for (int t0 = blockIdx.x * kCacheTokens; t0 < p.s.num_tokens; t0 += gridDim.x * kCacheTokens) {
+    __syncthreads();
+    place_tokens(p.c, p.s, t0, rows);
+    __syncthreads();
+    const int units = min(kCacheTokens, p.s.num_tokens - t0) * per_token;
+    for (int u = threadIdx.x; u < units; u += kCacheThreads) {
+      const int tk = u / per_token, r = u - tk * per_token;
+      const int c = r % C, kv = (r / C) / p.c.heads, h = (r / C) - kv * p.c.heads;
+      const int64_t row = rows[tk];
+      if (row == kRowNone) continue;
+      uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+      if (row >= 0) {
+        const int64_t at = row + (static_cast<int64_t>(h) << p.c.page_shift);
+        const uint8_t* base = kv == 0 ? p.c.k : p.c.v;
+        if (FMT == kCacheBf16) {
+          const uint4* src = reinterpret_cast<const uint4*>(base + at * (D * 2) + c * 32);
+          a = src[0];
+          b = src[1];
+        } else {
+          const uint8_t* sc = kv == 0 ? p.c.k_scale : p.c.v_scale;
+          const uint4 w = *reinterpret_cast<const uint4*>(base + at * D + c * 16);
+          dequant16<FMT>(w, sc[at * (D / kCacheGroup) + (c >> 1)], a, b);
+        }
+      }
+      __nv_bfloat16* dst = kv == 0 ? p.k + (t0 + tk) * p.k_token + h * p.k_head
+                                   : p.v + (t0 + tk) * p.v_token + h * p.v_head;
+      reinterpret_cast<uint4*>(dst + c * 16)[0] = a;
+      reinterpret_cast<uint4*>(dst + c * 16)[1] = b;
+    }
+  }
+}
+
+}  // namespace dynrad

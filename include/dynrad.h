@@ -16,6 +16,9 @@
  *      blocks, Eqs. 12-13 with epsilon -> 0, returning O and the log-sum-exp.
  *      dynrad_attn_backward is its gradient (dQ, dK, dV) under the same mask.
  *
+ * Beside them stands a paged K / V cache (dynrad_cache_write, dynrad_cache_read,
+ * dynrad_cache_attn) for sequences that grow piece by piece.
+ *
  * Conventions shared by every call
  *   - Pointers named q, k, v, o, lse, *_row_ptr, *_col*, forced_*, scores_out,
  *     workspace are DEVICE pointers owned by the caller.  Geometry structs and
@@ -455,6 +458,133 @@ int dynrad_attn_backward(const void *q, const void *k, const void *v,
                          const int32_t *col_idx, int64_t col_cap, float scale,
                          void *dq, void *dk, void *dv, void *workspace,
                          size_t workspace_bytes, dynrad_stream_t stream);
+
+/*
+ * Paged K / V cache (no counterpart in the paper: for callers that produce a
+ * video, or any sequence, piece by piece and attend over what came before).
+ *
+ * The cache is a pool of pages owned by the caller.  A page holds `page` tokens
+ * of every K / V head; formats:
+ *   DYNRAD_CACHE_BF16  k, v bf16 [num_pages, heads, page, dim]; no scales
+ *   DYNRAD_CACHE_E4M3  k, v e4m3 bytes of that shape and
+ *   DYNRAD_CACHE_INT8  k, v int8 of that shape, both with k_scale, v_scale
+ *                      uint8 [num_pages, heads, page, dim / 32]: one scale
+ *                      2^(byte - 127) for every 32 channels of a token
+ * A stored channel stands for code * scale, an exact bf16 number.  Writing 32
+ * channels of largest magnitude a stores the least scale 2^e, e >= -117, with
+ * a <= 448 * 2^e (e4m3) or 127 * 2^e (int8), and each channel over it rounded to
+ * nearest even: off by at most half a step (magnitudes over 240 * 2^120 for e4m3
+ * and 127 * 2^121 for int8 are stored as those).  An infinity or NaN among the 32
+ * stores the byte 255, and all 32 stand for NaN.  The pages hold what
+ * dynrad_cache_write stores (e4m3's own NaN codes are never among it).
+ */
+typedef enum dynrad_cache_format {
+  DYNRAD_CACHE_BF16 = 0,
+  DYNRAD_CACHE_E4M3 = 1,
+  DYNRAD_CACHE_INT8 = 2
+} dynrad_cache_format;
+
+typedef struct dynrad_kv_cache {
+  void *k;          /* DEVICE, 16-byte aligned */
+  void *v;          /* DEVICE, 16-byte aligned */
+  uint8_t *k_scale; /* DEVICE, 16-byte aligned; ignored for bf16 */
+  uint8_t *v_scale;
+  int64_t num_pages; /* num_pages * heads * page < 2^31 */
+  int32_t heads;     /* K / V heads */
+  int32_t page;      /* tokens a page: 16, 32, 64 or 128 */
+  int32_t dim;       /* 64 or 128 */
+  int32_t format;    /* dynrad_cache_format */
+} dynrad_kv_cache;
+
+/*
+ * The sequences of a call.  Sequence s has the tokens cu_seq[s] .. cu_seq[s+1] - 1
+ * of the call's num_tokens rows, n_s of them, and kv_len[s] positions in the
+ * cache WITH them: its token i stands at position kv_len[s] - n_s + i.  Position
+ * x lies in page page_table[s * table_stride + x / page], slot x % page.  The
+ * same three arrays serve all three calls below.  n_s may be 0, and may exceed
+ * kv_len[s]: positions below 0 are not written, read as zeros, and see nothing
+ * (with frame = 0: see what the others see).  Rows at or behind cu_seq[num_seqs]
+ * belong to nobody and are left as they were in every output.
+ * Values that lead out of the caller's arrays (cu_seq not ascending within
+ * [0, num_tokens], kv_len outside [0, max_pages * page], a page outside
+ * [0, num_pages)) are held inside them and recorded in the device status as
+ * DYNRAD_ERR_DEVICE: such a page is not written and reads as zeros.  Entries of
+ * the table behind a sequence's last position are never looked at.
+ */
+typedef struct dynrad_seqs {
+  const int32_t *page_table; /* DEVICE int32 [num_seqs rows of table_stride] */
+  const int32_t *cu_seq;     /* DEVICE int32 [num_seqs + 1] */
+  const int32_t *kv_len;     /* DEVICE int32 [num_seqs] */
+  int64_t table_stride;      /* >= max_pages */
+  int32_t num_seqs;          /* >= 0 */
+  int32_t max_pages;         /* pages a row of the table holds; max_pages * page < 2^31 */
+  int32_t num_tokens;        /* >= 0 */
+} dynrad_seqs;
+
+/*
+ * Writes K and V of the call's tokens at their positions, quantised to the
+ * cache's format (one kernel, one pass).
+ *
+ *   k, v          DEVICE bf16, 16-byte aligned: channel c of head h of token t at
+ *                 t * token_stride + h * head_stride + c (strides in elements,
+ *                 multiples of 8), so [T, H, D] and [H, T, D] both serve
+ * Two tokens of one call that name the same slot leave it undefined.
+ * Errors: DYNRAD_ERR_INVALID_ARG / UNSUPPORTED before any launch.
+ */
+int dynrad_cache_write(const dynrad_kv_cache *cache, const dynrad_seqs *seqs,
+                       const void *k, int64_t k_token_stride,
+                       int64_t k_head_stride, const void *v,
+                       int64_t v_token_stride, int64_t v_head_stride,
+                       dynrad_stream_t stream);
+
+/*
+ * The reverse: what the cache holds at the call's tokens' positions, as bf16
+ * (exactly what is stored).  With one sequence, cu_seq = {0, kv_len} and
+ * head-major strides it gives the [1, H, N, D] tensors of dynrad_select_blocks
+ * and dynrad_sparse_attn.  Arguments as above; k and v are written.
+ */
+int dynrad_cache_read(const dynrad_kv_cache *cache, const dynrad_seqs *seqs,
+                      void *k, int64_t k_token_stride, int64_t k_head_stride,
+                      void *v, int64_t v_token_stride, int64_t v_head_stride,
+                      dynrad_stream_t stream);
+
+/*
+ * Attention of the call's tokens over the cache (their own K and V written
+ * before).  Query head h uses K / V head h / (heads / cache->heads).  The token
+ * at position x of a sequence sees
+ *   frame = 0             every position 0 .. kv_len - 1
+ *   frame >= 1, window 0  positions below (floor(x / frame) + 1) * frame: its
+ *                         own frame and all before it (frame = 1: token-causal)
+ *   frame >= 1, window w  of those the last w frames, its own among them
+ * and over what it sees
+ *   o   = sum softmax(scale * q.k) v,   lse = ln sum exp(scale * q.k)
+ * with the tensor cores (tcgen05, bf16 operands, fp32 accumulation, P rounded to
+ * bf16) and an fp32 softmax.  A row that sees nothing, or whose logits are all
+ * -inf, gives o = 0 and lse = -inf.  What a row does not see cannot reach it,
+ * whatever it holds (NaN, infinity, memory never written).  lse is that of
+ * dynrad_sparse_attn, so parts of one row's keys can be joined by it.
+ *
+ *   q, o          DEVICE bf16, 16-byte aligned; strides in elements, multiples of
+ *                 8, as in dynrad_cache_write; o must not overlap q
+ *   heads         query heads, a multiple of cache->heads, at most 128 to each
+ *   scale         logit scale; 0 means 1/sqrt(dim)
+ *   lse           DEVICE fp32 [heads, num_tokens]
+ *   workspace     DEVICE, 256-byte aligned, at least
+ *                 dynrad_cache_attn_workspace_bytes(...) bytes (0 if it can not
+ *                 be sized); its contents do not matter and none are kept.
+ *                 Calls that overlap on the GPU need a workspace each.
+ * Errors: DYNRAD_ERR_INVALID_ARG / UNSUPPORTED / CAPACITY before any launch.
+ */
+size_t dynrad_cache_attn_workspace_bytes(const dynrad_kv_cache *cache,
+                                         int32_t num_seqs, int32_t num_tokens,
+                                         int32_t heads);
+int dynrad_cache_attn(const dynrad_kv_cache *cache, const dynrad_seqs *seqs,
+                      const void *q, int64_t q_token_stride,
+                      int64_t q_head_stride, int32_t heads, int32_t frame,
+                      int32_t window, float scale, void *o,
+                      int64_t o_token_stride, int64_t o_head_stride, float *lse,
+                      void *workspace, size_t workspace_bytes,
+                      dynrad_stream_t stream);
 
 /*
  * Reads the device status word (the first error a kernel recorded since the

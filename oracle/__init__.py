@@ -24,6 +24,8 @@ from "DynamicRad: Content-Adaptive Sparse Attention for Long Video Diffusion"
   fallback, aggregated to blocks;
 * ``backward``  -- gradients dQ, dK, dV of the block-masked attention (for the
   mask-aware fine-tuning of Sec. 3.3);
+* ``cache``     -- the paged K / V cache: its quantisation and the attention of
+  new tokens over it (no counterpart in the paper);
 * ``proxy``     -- the objective of the offline parameter search on the
   feature-drift proxy (Appendix C.2-C.4, Eq. 22).
 
