@@ -1123,7 +1123,7 @@ int check_cache(const dynrad_kv_cache* c, const dynrad_seqs* s, CacheDev* cd, Se
     return DYNRAD_ERR_INVALID_ARG;
   if (s->num_seqs < 0 || s->num_tokens < 0 || s->max_pages < 0 || s->table_stride < s->max_pages)
     return DYNRAD_ERR_INVALID_ARG;
-  if (s->max_pages > INT32_MAX / c->page) return DYNRAD_ERR_UNSUPPORTED;
+  if (s->max_pages > (INT32_MAX - 255) / c->page) return DYNRAD_ERR_UNSUPPORTED;
   if (s->num_seqs > 0 && (s->page_table == nullptr || s->cu_seq == nullptr || s->kv_len == nullptr))
     return DYNRAD_ERR_INVALID_ARG;
   cd->k = static_cast<uint8_t*>(c->k);
@@ -1221,12 +1221,109 @@ extern "C" int dynrad_cache_read(const dynrad_kv_cache* cache, const dynrad_seqs
   return launch_status();
 }
 
+namespace {
+
+// How a call of the cache's attention is laid out on the GPU (cacheattn.cuh).
+struct CachePlan {
+  int32_t group, tile_tokens, tiles, item_tokens, slots;
+  bool split;
+  size_t part_ml, part_desc, total;
+};
+
+constexpr int kCacheMaxPlan = 2048;   // places a CTA scans at its start
+
+int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, int32_t heads, CachePlan* pl) {
+  if (heads < 1 || c->heads < 1 || heads % c->heads != 0) return DYNRAD_ERR_INVALID_ARG;
+  pl->group = heads / c->heads;
+  if (pl->group > 128) return DYNRAD_ERR_UNSUPPORTED;
+  pl->tile_tokens = 128 / pl->group;
+  // one tile an item where the sequences' tokens fill no more on average
+  pl->tiles = static_cast<int64_t>(num_tokens) <= static_cast<int64_t>(num_seqs) * pl->tile_tokens ? 1 : 2;
+  pl->item_tokens = pl->tiles * pl->tile_tokens;
+  const int64_t slots = static_cast<int64_t>(num_tokens) / pl->item_tokens + num_seqs;
+  if (slots > INT32_MAX || c->heads > 65535) return DYNRAD_ERR_UNSUPPORTED;
+  pl->slots = static_cast<int32_t>(slots);
+  // The even cut pays while items are few or single sequences may be most of the
+  // work; full items in many waves leave little to even out, and keep a head's
+  // keys in L2 when they run head after head.
+  const bool many = slots * c->heads >= 8 * kCacheMaxCtas &&
+                    static_cast<int64_t>(num_tokens) >= static_cast<int64_t>(num_seqs) * pl->item_tokens;
+  pl->split = slots <= kCacheMaxPlan && !many;
+  const size_t rows = static_cast<size_t>(2) * kCacheMaxCtas * 128 * pl->tiles;
+  pl->part_ml = pl->split ? align256(rows * c->dim * 4) : 0;
+  pl->part_desc = pl->split ? align256(pl->part_ml + rows * 8) : 0;
+  pl->total = pl->split ? align256(pl->part_desc + 2 * kCacheMaxCtas * 16) : 256;
+  return DYNRAD_OK;
+}
+
+// bf16 K or V pages as rows of D, one a (page, head, slot); box = 64 columns x a page.
+bool encode_pages(CUtensorMap* map, const void* base, const dynrad_kv_cache* c) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(c->dim), static_cast<cuuint64_t>(c->num_pages) * c->heads * c->page};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(c->dim) * 2};
+  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(c->page)};
+  cuuint32_t es[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Q as [D, heads, tokens] with the caller's strides; box = 64 columns x one tile's
+// heads and tokens, which land as its rows in order.
+bool encode_cache_q(CUtensorMap* map, const void* q, int D, int heads, int tokens, int64_t head_stride,
+                    int64_t token_stride, int group, int tile_tokens) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(token_stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tile_tokens)};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int FMT, int QT>
+int launch_cache_attn(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
+                      int ctas, cudaStream_t st) {
+  using C = CacheAttnCfg<D, FMT, QT>;
+  static OptInTable optin;   // per instantiation, per device
+  const int rc = smem_optin(optin, reinterpret_cast<const void*>(cache_attn_kernel<D, FMT, QT>), C::kSmem);
+  if (rc != DYNRAD_OK) return rc;
+  const dim3 grid = p.split ? dim3(ctas) : dim3(p.slots, p.c.heads);
+  cache_attn_kernel<D, FMT, QT><<<grid, C::kThreads, C::kSmem, st>>>(mq, mk, mv, p);
+  return launch_status();
+}
+
+template <int D>
+int launch_cache_join(const CacheAttnParams& p, const CachePlan& pl, int ctas, cudaStream_t st) {
+  // the launch overlaps the end of the attention; the kernel waits for all of it
+  const int per_cta = 256 / (D / 4);
+  const int rows = std::min(pl.item_tokens, p.s.num_tokens) * pl.group;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, std::min(8, (rows + per_cta - 1) / per_cta));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, p, pl.item_tokens, 128 * pl.tiles, ctas) != cudaSuccess)
+    return DYNRAD_ERR_CUDA;
+  return launch_status();
+}
+
+}  // namespace
+
 extern "C" size_t dynrad_cache_attn_workspace_bytes(const dynrad_kv_cache* cache, int32_t num_seqs,
                                                     int32_t num_tokens, int32_t heads) {
-  if (cache == nullptr || num_seqs < 0 || num_tokens < 0 || heads < 1 || cache->heads < 1 ||
-      heads % cache->heads != 0 || (cache->dim != 64 && cache->dim != 128))
+  CachePlan pl;
+  if (cache == nullptr || num_seqs < 0 || num_tokens < 0 || (cache->dim != 64 && cache->dim != 128) ||
+      cache_plan(cache, num_seqs, num_tokens, heads, &pl) != DYNRAD_OK)
     return 0;
-  return 256;
+  return pl.total;
 }
 
 extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs* seqs, const void* q,
@@ -1234,36 +1331,56 @@ extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs
                                  int32_t window, float scale, void* o, int64_t o_token_stride, int64_t o_head_stride,
                                  float* lse, void* workspace, size_t workspace_bytes, dynrad_stream_t stream) {
   CacheAttnParams p;
+  CachePlan pl;
   int rc = check_cache(cache, seqs, &p.c, &p.s);
   if (rc != DYNRAD_OK) return rc;
-  if (heads < 1 || heads % cache->heads != 0 || frame < 0 || window < 0 || (frame == 0 && window > 0))
-    return DYNRAD_ERR_INVALID_ARG;
+  if (frame < 0 || window < 0 || (frame == 0 && window > 0)) return DYNRAD_ERR_INVALID_ARG;
   if (!(scale >= 0.0f) || !std::isfinite(scale)) return DYNRAD_ERR_INVALID_ARG;
-  if (heads / cache->heads > 128) return DYNRAD_ERR_UNSUPPORTED;
+  if ((rc = cache_plan(cache, p.s.num_seqs, p.s.num_tokens, heads, &pl)) != DYNRAD_OK) return rc;
   if (p.s.num_seqs == 0 || p.s.num_tokens == 0) return DYNRAD_OK;
   if (bad_rows(q, q_token_stride, q_head_stride) || bad_rows(o, o_token_stride, o_head_stride) || lse == nullptr ||
       workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return DYNRAD_ERR_INVALID_ARG;
-  if (workspace_bytes < dynrad_cache_attn_workspace_bytes(cache, seqs->num_seqs, seqs->num_tokens, heads))
-    return DYNRAD_ERR_CAPACITY;
+  if ((heads > 1 && q_head_stride == 0) || (p.s.num_tokens > 1 && q_token_stride == 0)) return DYNRAD_ERR_INVALID_ARG;
+  if (workspace_bytes < pl.total) return DYNRAD_ERR_CAPACITY;
   const float sc = scale == 0.0f ? 1.0f / std::sqrt(static_cast<float>(cache->dim)) : scale;
-  p.q = static_cast<const __nv_bfloat16*>(q);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  p.q_token = q_token_stride;
-  p.q_head = q_head_stride;
   p.o_token = o_token_stride;
   p.o_head = o_head_stride;
-  p.heads = heads;
-  p.group = heads / cache->heads;
+  p.group = pl.group;
+  p.tile_tokens = pl.tile_tokens;
   p.frame = frame;
   p.window = window;
+  p.slots = pl.slots;
+  p.split = pl.split ? 1 : 0;
   p.scale_log2 = sc * 1.4426950408889634f;
-  const int64_t rows = static_cast<int64_t>(seqs->num_tokens) * heads;
-  if ((rows + 3) / 4 > INT32_MAX) return DYNRAD_ERR_UNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-#define DYNRAD_CACHE_F(D_, F_) cache_attn_kernel<D_, F_><<<grid, 128, 0, as_stream(stream)>>>(p)
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + pl.part_ml);
+  p.part_desc = reinterpret_cast<int4*>(ws + pl.part_desc);
+  const uint64_t wl = g_attn_wait_ns.load(std::memory_order_relaxed);
+  p.wait_ns = wl != 0 ? wl : kWaitLimitNs;
+  p.stall_step = g_attn_stall_step.load(std::memory_order_relaxed);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DYNRAD_ERR_CUDA;
+  const int ctas = std::min(sms, kCacheMaxCtas);
+  CUtensorMap mq = {}, mk = {}, mv = {};
+  const int64_t any = cache->dim;   // stride of an axis of length one: any that the map takes
+  if (!encode_cache_q(&mq, q, cache->dim, heads, p.s.num_tokens, heads > 1 ? q_head_stride : any,
+                      p.s.num_tokens > 1 ? q_token_stride : any, pl.group, pl.tile_tokens))
+    return DYNRAD_ERR_CUDA;
+  if (cache->format == DYNRAD_CACHE_BF16 &&
+      (!encode_pages(&mk, cache->k, cache) || !encode_pages(&mv, cache->v, cache)))
+    return DYNRAD_ERR_CUDA;
+  cudaStream_t st = as_stream(stream);
+#define DYNRAD_CACHE_F(D_, F_)                                                     \
+  rc = pl.tiles == 1 ? launch_cache_attn<D_, F_, 1>(mq, mk, mv, p, ctas, st)       \
+                     : launch_cache_attn<D_, F_, 2>(mq, mk, mv, p, ctas, st)
   DYNRAD_CACHE_DISPATCH(cache->dim, cache->format, DYNRAD_CACHE_F);
 #undef DYNRAD_CACHE_F
-  return launch_status();
+  if (rc != DYNRAD_OK || !pl.split) return rc;
+  return cache->dim == 128 ? launch_cache_join<128>(p, pl, ctas, st) : launch_cache_join<64>(p, pl, ctas, st);
 }

@@ -517,7 +517,7 @@ typedef struct dynrad_seqs {
   const int32_t *kv_len;     /* DEVICE int32 [num_seqs] */
   int64_t table_stride;      /* >= max_pages */
   int32_t num_seqs;          /* >= 0 */
-  int32_t max_pages;         /* pages a row of the table holds; max_pages * page < 2^31 */
+  int32_t max_pages;         /* pages a row of the table holds; max_pages * page < 2^31 - 255 */
   int32_t num_tokens;        /* >= 0 */
 } dynrad_seqs;
 
@@ -605,8 +605,8 @@ int dynrad_debug_exp2(const float *x, float *poly_out, float *ref_out,
                       int64_t n, dynrad_stream_t stream);
 
 /*
- * Test hook for the attention forward's failure path (no counterpart in the
- * paper), for launches made after the call:
+ * Test hook for the failure path of the attention forward and of the cache's
+ * attention (no counterpart in the paper), for launches made after the call:
  *   wait_ns     limit, in nanoseconds of the GPU's global timer, of the
  *               kernel's pipeline waits; 0 restores the built-in limit (2 s)
  *   stall_step  >= 0: at that step of its walk the MMA warp of every CTA waits

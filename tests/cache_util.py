@@ -124,4 +124,4 @@ def check_attention(o, lse, q, kept_k, kept_v, b, frame, window, scale=None):
             assert np.array_equal(np.isnan(lref), np.isnan(lgot))
             live = np.isfinite(lref)
             ltol = 2 * slack + 4 * U_FP32 * np.abs(np.where(live, lref, 0.0))
-            assert (np.abs(lgot - lref)[live] <= ltol[live]).all(), (s, h, np.abs(lgot - lref)[live].max())
+            assert (np.abs(lgot[live] - lref[live]) <= ltol[live]).all(), (s, h, np.abs(lgot[live] - lref[live]).max())

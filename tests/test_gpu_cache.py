@@ -152,6 +152,63 @@ def test_attention_matches_the_oracle(fmt, dim, name, heads, kv_heads, page, fra
     assert (o[b.cu_np[-1]:] == 7.0).all() and (lse[:, b.cu_np[-1]:] == 7.0).all()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("ns,lens,heads,kv_heads,dim,page,frame,window", [
+    ([1], [9000], 4, 1, 128, 16, 1, 0),                      # one item cut into many parts
+    ([1, 1, 1], [5000, 1, 2600], 8, 2, 64, 32, 1, 700),
+    ([2, 600], [4000, 1500], 2, 2, 128, 64, 1, 0),           # two tiles an item, parts of both
+    ([300], [2500], 10, 2, 64, 128, 100, 4),
+    ([257, 1, 255], [700, 900, 255], 3, 3, 128, 32, 0, 0),
+])
+def test_items_cut_into_parts(fmt, ns, lens, heads, kv_heads, dim, page, frame, window):
+    b = Batch(ns, lens, page, seed=len(lens))
+    g = gen(page + heads)
+    c, kk, kv = filled_cache(b, kv_heads, dim, fmt, g)
+    q = torch.randn((b.tokens, heads, dim), generator=g, device="cuda").bfloat16()
+    o, lse = abi.dynrad_cache_attn(q, c, *b.call(), frame=frame, window=window)
+    torch.cuda.synchronize()
+    check_device_status()
+    check_attention(o, lse, q, kk, kv, b, frame, window)
+    o2, lse2 = abi.dynrad_cache_attn(q, c, *b.call(), frame=frame, window=window)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("ns,lens,heads,kv_heads", [
+    ([1700], [1750], 192, 12),              # items in many waves: one to a CTA
+    ([900, 1, 830, 0, 60], [950, 70, 830, 5, 300], 192, 12),
+    ([1] * 2100, [1 + i % 37 for i in range(2100)], 2, 1),      # more places than a CTA scans
+])
+def test_calls_of_many_items(ns, lens, heads, kv_heads):
+    b = Batch(ns, lens, 32, seed=1)
+    g = gen(len(ns))
+    c, kk, kv = filled_cache(b, kv_heads, 64, "int8", g)
+    q = torch.randn((b.tokens, heads, 64), generator=g, device="cuda").bfloat16()
+    o, lse = abi.dynrad_cache_attn(q, c, *b.call())
+    torch.cuda.synchronize()
+    check_device_status()
+    check_attention(o, lse, q, kk, kv, b, 1, 0)
+
+
+def test_a_wait_that_runs_out_is_recorded_and_the_next_call_is_right():
+    b = Batch([1, 200], [800, 700], 64, seed=3)
+    g = gen(6)
+    for fmt in FORMATS:
+        c, kk, kv = filled_cache(b, 2, 128, fmt, g)
+        q = torch.randn((b.tokens, 4, 128), generator=g, device="cuda").bfloat16()
+        check_device_status()
+        abi.dynrad_debug_attn_stall(20_000, 1)
+        try:
+            abi.dynrad_cache_attn(q, c, *b.call())
+            torch.cuda.synchronize()
+        finally:
+            abi.dynrad_debug_attn_stall()
+        assert abi.dynrad_device_status(clear=True) == abi.DYNRAD_ERR_DEVICE
+        o, lse = abi.dynrad_cache_attn(q, c, *b.call())
+        torch.cuda.synchronize()
+        check_device_status()
+        check_attention(o, lse, q, kk, kv, b, 1, 0)
+
+
 @pytest.mark.parametrize("heads,kv_heads", [(7, 1), (12, 4), (40, 8), (128, 1), (3, 3)])
 def test_head_groups_and_layouts(heads, kv_heads):
     b = Batch([3, 150, 1], [200, 150, 90], 32, seed=5)
@@ -206,6 +263,8 @@ def test_what_a_row_does_not_see_cannot_reach_it(fmt, frame, window, bad):
             t = int(b.cu_np[s]) + i
             if lo <= pos < hi:
                 assert not torch.isfinite(o[t, :, 5]).any()
+                group = 1 if fmt == "bf16" else 32       # what shares the bad channel's scale
+                assert torch.equal(o[t, :, group if group > 1 else 6:], o_ref[t, :, group if group > 1 else 6:])
                 if fmt == "bf16" and math.isinf(bad):
                     assert (o[t, :, 5] == bad).all()
             else:
