@@ -35,7 +35,7 @@
 //              Q by TMA (a [D, heads, tokens] map: any strides) and each step's K
 //              and V pages, one lane a page.
 //   warp 9     MMA issuer: O_t += P_t V(j), then S_t = Q_t K(j+1)^T.
-//   warps 10-15 (8-bit pages) turn what was loaded into bf16 operand tiles.
+//   warps 12-19 (8-bit pages) turn what was loaded into bf16 operand tiles.
 //              Scales are powers of two, so those tiles are exact and everything
 //              behind them is the same for all formats.
 //
@@ -69,11 +69,15 @@ struct CacheAttnCfg {
   static constexpr int kBudget = 227 * 1024 - 1024 - kCtrl - QT * kTileBytes;   // 1024: manual alignment
   static constexpr bool kRaw = FMT != kCacheBf16;
   // 8-bit: three operand tiles (V(j), K(j+1), and the one being filled), the rest raw
-  static constexpr int kSlots = kRaw ? (D == 64 ? 4 : 3) : (kBudget / kTileBytes < 8 ? kBudget / kTileBytes : 8);
+  static constexpr int kSlots = kRaw ? (D == 64 || QT == 1 ? 4 : 3) : (kBudget / kTileBytes < 8 ? kBudget / kTileBytes : 8);
   static constexpr int kRawFit = kRaw ? (kBudget - kSlots * kTileBytes) / kRawBytes : 0;
   static constexpr int kRawSlots = kRawFit < 8 ? kRawFit : 8;
-  static constexpr int kDqWarps = kRaw ? 6 : 0;
-  static constexpr int kThreads = 320 + 32 * kDqWarps;
+  static constexpr int kDqWarps = kRaw ? 8 : 0;
+  static constexpr int kThreads = kRaw ? 640 : 320;
+  // 8-bit: registers a thread after the split by warpgroup (two of softmax, one of
+  // producer and MMA, two that dequantise); 640 threads start with 96
+  static constexpr int kRegsSoftmax = 144, kRegsOther = 64;
+  static_assert(256 * kRegsSoftmax + 384 * kRegsOther <= 640 * 96, "registers at launch");
   static constexpr int kSmem = QT * kTileBytes + kSlots * kTileBytes + kRawSlots * kRawBytes + kCtrl + 1024;
   static constexpr int kRows = 128 * QT;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -182,6 +186,15 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                    smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -297,7 +310,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
                 "control block");
   static_assert(kSegRing * sizeof(CacheSeg) % 8 == 0 && kSegRing % 2 == 0, "alignment of the control block");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint64_t wlim = p.wait_ns;
   const int item_tokens = QT * p.tile_tokens;
 
@@ -341,6 +354,281 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
   // waits for segment g of the CTA and gives it back when a warp is through with it
   auto seg_wait = [&](int g) -> bool { return mbar_wait(&seg_full[g % kSegRing], (g / kSegRing) & 1, abort_flag, wlim); };
 
+  if (warp < 8) {
+    if constexpr (C::kRaw) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+    // -------------------------------------------------------------- softmax
+    // Both 64-column halves unrolled for bf16 pages; looped over beside the
+    // dequantising warps, whose code shares the instruction cache (one 480p frame of
+    // 40 heads over 32,760 keys: e4m3 1.46 -> 1.43 ms looped, bf16 1.26 -> 1.32).
+    constexpr int kHalves = C::kRaw ? 1 : 2;
+    const int tile = warp >> 2;
+    const int t = threadIdx.x - tile * 128;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t col_s = 256u + 128u * tile, col_o = 128u * tile;
+    const float c2 = p.scale_log2;
+    const int rtok = t / p.group, rhead = t - rtok * p.group;
+    int ns = 0, no = 0, nml = 0, li = 0;      // s_full and o_full phases, narrow joins, K / V tiles
+    bool ok = true;
+    for (int g = 0; ok; ++g) {
+      if (!__all_sync(0xffffffffu, seg_wait(g))) break;
+      const CacheSeg& sg = segs[g % kSegRing];
+      if (sg.end) break;
+      // this thread's row: in a narrow segment both warpgroups have the same rows
+      const int tok = rtok + (sg.narrow ? 0 : tile * p.tile_tokens);
+      const bool valid = rtok < p.tile_tokens && tok < sg.it.ntok;
+      int32_t lo = 0, hi = INT32_MAX;    // rows that are not there count as seeing all: nothing to mask
+      if (valid) seen_range(p.frame, p.window, sg.it.pos0 + tok, sg.it.len, lo, hi);
+      const bool warp_rows = __any_sync(0xffffffffu, valid);
+      const int sa = sg.sa, sb = sg.sb, step0 = sg.it.step0;
+      float m_used = -INFINITY, l = 0.f;
+      for (int j = sa; j < sb; ++j, li += 2) {
+        const int32_t key0 = (step0 + j) << 7;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[tile], ns & 1, abort_flag, wlim))) { ok = false; break; }
+        ++ns;
+        tc_fence_after();
+        if (!C::kRaw && tile == 0 && seg_partial(sg, j)) {
+          // thread = key: V rows that nobody sees, or that are not finite
+          if (!__all_sync(0xffffffffu,
+                          mbar_wait(&slot_full[(li + 1) % NS], ((li + 1) / NS) & 1, abort_flag, wlim))) {
+            ok = false;
+            break;
+          }
+          uint8_t* vrow = slot_smem + ((li + 1) % NS) * TB + t * 128;
+          const bool seen = key0 + t >= sg.it.lo && key0 + t < sg.it.hi;
+          bool bad = false;
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              uint4* at = reinterpret_cast<uint4*>(vrow + c * C::kChunkBytes + u * 16);
+              uint4 y = make_uint4(0u, 0u, 0u, 0u);
+              if (seen) {
+                const uint4 x = *at;
+                y = make_uint4(finite_bf16x2(x.x), finite_bf16x2(x.y), finite_bf16x2(x.z), finite_bf16x2(x.w));
+                if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
+                bad = true;
+              }
+              *at = y;
+            }
+          if (bad) poison[g % kSegRing] = g + 1;
+          fence_async_shared();
+        }
+        if (warp_rows && seg_active(sg, tile, j)) {
+          const int32_t rl = max(lo - key0, 0), rh = min(hi - key0, 128);   // columns [rl, rh) count
+          // of each 64-column half: all lanes see all of it, or none any
+          uint32_t half_full = 0, half_none = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (__all_sync(0xffffffffu, rl <= 64 * h && rh >= 64 * h + 64)) half_full |= 1u << h;
+            if (__all_sync(0xffffffffu, rl >= 64 * h + 64 || rh <= 64 * h)) half_none |= 1u << h;
+          }
+          float mx = -INFINITY;
+#pragma unroll kHalves
+          for (int h = 0; h < 2; ++h) {
+            if ((half_none >> h) & 1u) continue;
+            float sv[64];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t r[32];
+              tmem_ld32(taddr + lane_base + col_s + h * 64 + c * 32, r);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(r[i]);
+            }
+            tmem_wait_ld();
+            if ((half_full >> h) & 1u) {
+              float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int i = 0; i < 64; i += 8) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) m4[u] = fmax3(m4[u], sv[i + 2 * u], sv[i + 2 * u + 1]);
+              }
+              mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if (h * 64 + i >= rl && h * 64 + i < rh) mx = fmaxf(mx, sv[i]);
+            }
+          }
+          const float m_new = fmaxf(m_used, mx * c2);
+          const bool need = valid && m_used != -INFINITY && m_new > m_used + 8.0f;
+          if (__any_sync(0xffffffffu, need)) {
+            const float alpha = need ? ex2_approx(m_used - m_new) : 1.0f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32(taddr + lane_base + col_o + c * 32, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              tmem_st32(taddr + lane_base + col_o + c * 32, r);
+            }
+            if (need) {
+              l *= alpha;
+              m_used = m_new;
+            }
+          }
+          if (m_used == -INFINITY) m_used = m_new;
+          // a row whose logits so far are all -inf keeps 0 as its reference: every P is 0
+          const float ref = m_used == -INFINITY ? 0.f : m_used;
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 cc = make_float2(c2, c2), mm = make_float2(-ref, -ref);
+#pragma unroll kHalves
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+            if ((half_none >> h) & 1u) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) pk[i] = 0u;
+            } else {
+              float sv[64];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint32_t r[32];
+                tmem_ld32(taddr + lane_base + col_s + h * 64 + c * 32, r);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(r[i]);
+              }
+              tmem_wait_ld();
+              if (!((half_full >> h) & 1u)) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                  if (h * 64 + i < rl || h * 64 + i >= rh) sv[i] = -INFINITY;
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float2 x = __ffma2_rn(make_float2(sv[2 * i], sv[2 * i + 1]), cc, mm);
+                const float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                acc[i & 3] = __fadd2_rn(acc[i & 3], pe);
+                pk[i] = pack_bf16x2(pe.x, pe.y);
+              }
+            }
+            tmem_st32(taddr + lane_base + col_s + h * 32, pk);
+          }
+          const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+          l += a.x + a.y;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[tile]);
+      }
+      if (!ok) break;
+      // the last product into this tile's O
+      bool have = false, have1 = false;
+      if (sb > sa) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&o_full[tile], no & 1, abort_flag, wlim))) { ok = false; break; }
+        ++no;
+        tc_fence_after();
+        have = sg.narrow ? sb - sa > tile : max(sa, sg.act_a[tile]) < min(sb, sg.act_b[tile]);
+      }
+      float w0 = 1.f, w1 = 0.f;
+      if (sg.narrow && sb > sa) {
+        if (tile == 1) {
+          ml[t] = make_float2(m_used, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ml_full);
+          if (!__all_sync(0xffffffffu, mbar_wait(ml_done, nml & 1, abort_flag, wlim))) { ok = false; break; }
+        } else {
+          if (!__all_sync(0xffffffffu, mbar_wait(ml_full, nml & 1, abort_flag, wlim))) { ok = false; break; }
+          tc_fence_after();
+          if (sb - sa > 1) {
+            have1 = true;
+            const float2 b = ml[t];
+            const float m = fmaxf(m_used, b.x);
+            w0 = m_used == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_approx(m_used - m);
+            w1 = b.x == -INFINITY ? (b.y == 0.f ? 0.f : 1.f) : ex2_approx(b.x - m);
+            l = l * w0 + b.y * w1;
+            m_used = m;
+          }
+        }
+        ++nml;
+      }
+      if (warp_rows && !(sg.narrow && tile == 1)) {
+        const bool poisoned = poison[g % kSegRing] == g + 1;
+        const bool part = sg.part >= 0;
+        const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+        const int64_t token = sg.it.tok0 + tok;
+        const int qhead = sg.head * p.group + rhead;
+        __nv_bfloat16* orow = p.o + token * p.o_token + qhead * p.o_head;
+        const int64_t prow = part ? (2 * static_cast<int64_t>(blockIdx.x) + sg.part) * C::kRows +
+                                        (sg.narrow ? 0 : tile * 128) + t
+                                  : 0;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float x[32];
+          {
+            uint32_t r[32];
+            if (have) {
+              tmem_ld32(taddr + lane_base + col_o + c * 32, r);
+              tmem_wait_ld();
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = have && w0 != 0.f ? __uint_as_float(r[i]) * w0 : 0.f;
+            if (have1) {
+              tmem_ld32(taddr + lane_base + 128u + c * 32, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (w1 != 0.f) x[i] = fmaf(__uint_as_float(r[i]), w1, x[i]);
+            }
+          }
+          if (poisoned && valid) {
+            for (int j = sa; j < sb; ++j) {
+              if (!seg_partial(sg, j)) continue;
+              const int32_t key0 = (step0 + j) << 7;
+              for (int32_t key = max(lo, key0); key < min(hi, key0 + 128); ++key) {
+                const int64_t at = cache_row(p.c, p.s, sg.it.seq, key);
+                if (at < 0) continue;
+                const int64_t row = at + (static_cast<int64_t>(sg.head) << p.c.page_shift);
+                if (C::kRaw) {
+                  if (p.c.v_scale[row * (D / kCacheGroup) + c] == kCacheNanScale) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = __int_as_float(0x7fffffff);
+                  }
+                } else {
+                  const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.c.v) + row * D;
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    const float f = __bfloat162float(v[c * 32 + i]);
+                    if (!isfinite(f)) x[i] += f;
+                  }
+                }
+              }
+            }
+          }
+          if (valid) {
+            if (part) {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_uint4(pack_bf16x2(x[8 * i] * inv, x[8 * i + 1] * inv),
+                                    pack_bf16x2(x[8 * i + 2] * inv, x[8 * i + 3] * inv),
+                                    pack_bf16x2(x[8 * i + 4] * inv, x[8 * i + 5] * inv),
+                                    pack_bf16x2(x[8 * i + 6] * inv, x[8 * i + 7] * inv));
+            }
+          }
+        }
+        if (valid) {
+          if (part)
+            p.part_ml[prow] = make_float2(m_used, l);
+          else
+            p.lse[static_cast<int64_t>(qhead) * p.s.num_tokens + token] =
+                l == 0.f ? -INFINITY : m_used * 0.69314718055994531f + __logf(l);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (sg.narrow && sb > sa && tile == 0) mbar_arrive(ml_done);
+        mbar_arrive(&seg_empty[g % kSegRing]);
+      }
+    }
+  } else {
+    if constexpr (C::kRaw) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
   if (warp == 8) {
     // ------------------------------------------------------------- producer
     const int ps = p.c.page_shift, page = 1 << ps, npg = 128 >> ps;
@@ -522,86 +810,137 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
     __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
-      const uint64_t qdesc0 = smem_desc_sw128(smem_u32(q_smem), 16, 1024);
-      const uint64_t kdesc0 = smem_desc_sw128(smem_u32(slot_smem), 16, 1024);
-      const uint64_t vdesc0 = smem_desc_sw128(smem_u32(slot_smem), C::kChunkBytes, 1024);
-      auto desc_add = [](uint64_t d, uint32_t bytes) -> uint64_t { return d + (bytes >> 4); };
-      bool ok = true;
-      int nq = 0, li = 0, np = 0, nsteps = 0;
-      for (int g = 0; ok; ++g) {
-        if (!seg_wait(g)) break;
-        const CacheSeg sg = segs[g % kSegRing];
-        mbar_arrive(&seg_empty[g % kSegRing]);
-        if (sg.end) break;
-        if (sg.sb <= sg.sa) continue;
-        const uint32_t q1 = sg.narrow ? 0u : static_cast<uint32_t>(TB);   // tile 1's rows
-        bool started[2] = {false, false};
-        auto issue_qk = [&](int t, int i) {
-          const uint64_t ad = desc_add(qdesc0, t * q1);
-          const uint64_t bd = desc_add(kdesc0, (i % NS) * TB);
-          const uint32_t d = taddr + 256u + 128u * t;
+    // The whole warp runs the loop and one lane issues: what the products' operands
+    // are made from stays the same in all lanes, so it lives in uniform registers
+    // and an issue costs little beside the product itself.
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
+    const uint64_t qdesc0 = smem_desc_sw128(smem_u32(q_smem), 16, 1024);
+    const uint64_t kdesc0 = smem_desc_sw128(smem_u32(slot_smem), 16, 1024);
+    const uint64_t vdesc0 = smem_desc_sw128(smem_u32(slot_smem), C::kChunkBytes, 1024);
+    auto desc_add = [](uint64_t d, uint32_t bytes) -> uint64_t { return d + (bytes >> 4); };
+    auto uniform = [](int x) -> int { return __shfl_sync(0xffffffffu, x, 0); };
+    const bool leader = elect_one();
+    bool ok = true;
+    int nq = 0, li = 0, np = 0, nsteps = 0;
+    auto wait = [&](uint64_t* b, int phase) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(b, phase & 1, abort_flag, wlim));
+    };
+    auto full = [&](int i) -> bool { return wait(&slot_full[i % NS], i / NS); };
+    auto commit = [&](uint64_t* b) {
+      if (leader) mma_commit(b);
+    };
+    // S_t = Q_t K^T (a narrow segment's tiles share Q_0); O_t += P_t V, or = for the
+    // tile's first product of a segment
+    auto issue_qk = [&](uint32_t d, uint64_t ad, int i) {
+      const uint64_t bd = desc_add(kdesc0, (i % NS) * TB);
+      if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const int c = kk >> 2, off = (kk & 3) * 32;
-            mma_ss(d, desc_add(ad, c * C::kChunkBytes + off), desc_add(bd, c * C::kChunkBytes + off), idesc_qk,
-                   kk > 0 ? 1u : 0u);
-          }
-        };
-        auto issue_pv = [&](int t, int i) {
-          const uint64_t bd = desc_add(vdesc0, (i % NS) * TB);
-          const uint32_t d = taddr + 128u * t, a = taddr + 256u + 128u * t;
-          const uint32_t acc0 = started[t] ? 1u : 0u;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_ts(d, a + kk * 8, desc_add(bd, kk * 2048), idesc_pv, kk > 0 ? 1u : acc0);
-          started[t] = true;
-        };
-        auto full = [&](int i) { return mbar_wait(&slot_full[i % NS], (i / NS) & 1, abort_flag, wlim); };
-        if (!mbar_wait(q_full, nq & 1, abort_flag, wlim) || !full(li)) break;
-        ++nq;
-        tc_fence_after();
-        for (int t = 0; t < 2; ++t) {
-          if (seg_active(sg, t, sg.sa)) issue_qk(t, li);
-          mma_commit(&s_full[t]);
-        }
-        mma_commit(&slot_empty[li % NS]);
-        if (sg.sb == sg.sa + 1) mma_commit(q_empty);
-        for (int j = sg.sa; j < sg.sb; ++j) {
-          const int iv = li + 1, ik = li + 2;
-          const bool more = j + 1 < sg.sb;
-          if (nsteps++ == p.stall_step && !mbar_wait(stall, 0, abort_flag, wlim)) { ok = false; break; }
-          if (!full(iv) || (more && !full(ik))) { ok = false; break; }
-          tc_fence_after();
-          for (int t = 0; t < 2; ++t) {
-            if (!mbar_wait(&p_full[t], np & 1, abort_flag, wlim)) { ok = false; break; }
-            tc_fence_after();
-            if (seg_active(sg, t, j)) issue_pv(t, iv);
-            if (more && seg_active(sg, t, j + 1)) issue_qk(t, ik);
-            if (t == 1) {
-              mma_commit(&slot_empty[iv % NS]);
-              if (more) mma_commit(&slot_empty[ik % NS]);
-              if (j + 2 == sg.sb) mma_commit(q_empty);
-            }
-            // the next segment's first S may follow before the softmax has seen this
-            // one's last product, so that one has a barrier of its own
-            mma_commit(more ? &s_full[t] : &o_full[t]);
-          }
-          if (!ok) break;
-          ++np;
-          li += 2;
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int c = kk >> 2, off = (kk & 3) * 32;
+          mma_ss(d, desc_add(ad, c * C::kChunkBytes + off), desc_add(bd, c * C::kChunkBytes + off), idesc_qk,
+                 kk > 0 ? 1u : 0u);
         }
       }
-      // all issued tensor-core work finished before tensor memory is released
-      mma_commit(drain);
-      mbar_wait(drain, 0, nullptr);
+    };
+    auto issue_pv = [&](uint32_t d, uint32_t a, int i, uint32_t acc0) {
+      const uint64_t bd = desc_add(vdesc0, (i % NS) * TB);
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_ts(d, a + kk * 8, desc_add(bd, kk * 2048), idesc_pv, kk > 0 ? 1u : acc0);
+      }
+    };
+    const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(taddr)));
+    const uint32_t s0 = tm + 256u, s1 = tm + 384u, o0 = tm, o1 = tm + 128u;
+    for (int g = 0; ok; ++g) {
+      if (!wait(&seg_full[g % kSegRing], g / kSegRing)) break;
+      const CacheSeg& sr = segs[g % kSegRing];
+      const int n = uniform(sr.sb - sr.sa);
+      const bool end = uniform(sr.end), narrow = uniform(sr.narrow);
+      // steps, counted from the segment's first, in which the tiles see something
+      const int a0 = uniform(sr.act_a[0] - sr.sa), b0 = uniform(sr.act_b[0] - sr.sa);
+      const int a1 = uniform(sr.act_a[1] - sr.sa), b1 = uniform(sr.act_b[1] - sr.sa);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[g % kSegRing]);
+      if (end) break;
+      if (n <= 0) continue;
+      if (!wait(q_full, nq) || !full(li)) break;
+      ++nq;
+      tc_fence_after();
+      const uint64_t q0 = qdesc0, q1 = desc_add(qdesc0, TB);
+      uint32_t acc0 = 0u, acc1 = 0u;
+      if (narrow || (a0 <= 0 && b0 > 0)) issue_qk(s0, q0, li);
+      commit(&s_full[0]);
+      if (!narrow && a1 <= 0 && b1 > 0) issue_qk(s1, q1, li);
+      commit(&s_full[1]);
+      commit(&slot_empty[li % NS]);
+      if (n == 1) commit(q_empty);
+      // At a segment's last step the next one's first S may follow before the softmax
+      // has seen this one's last product, so that one has a barrier of its own.
+      for (int j = 0; ok && j < n; ++j, ++np, li += 2) {
+        const int iv = li + 1, ik = li + 2;
+        const bool more = j + 1 < n;
+        ok = false;
+        if (nsteps++ == p.stall_step && !wait(stall, 0)) break;
+        if (more && !full(ik)) break;
+        if (!narrow) {
+          // both tiles' waits but the softmax's come first: each tile's products go
+          // out back to back
+          const bool v0 = j >= a0 && j < b0, v1 = j >= a1 && j < b1;
+          const bool k0 = more && j + 1 >= a0 && j + 1 < b0, k1 = more && j + 1 >= a1 && j + 1 < b1;
+          if (!full(iv) || !wait(&p_full[0], np)) break;
+          tc_fence_after();
+          if (v0) issue_pv(o0, s0, iv, acc0), acc0 = 1u;
+          if (k0) issue_qk(s0, q0, ik);
+          commit(more ? &s_full[0] : &o_full[0]);
+          if (!wait(&p_full[1], np)) break;
+          tc_fence_after();
+          if (v1) issue_pv(o1, s1, iv, acc1), acc1 = 1u;
+          if (k1) issue_qk(s1, q1, ik);
+          commit(&slot_empty[iv % NS]);
+          if (more) commit(&slot_empty[ik % NS]);
+          if (j + 2 == n) commit(q_empty);
+          commit(more ? &s_full[1] : &o_full[1]);
+        } else {
+          // the idle tile's next S first: it does not wait for this step's softmax
+          const int t = j & 1;
+          const uint32_t s_t = t ? s1 : s0, s_i = t ? s0 : s1;
+          if (!wait(&p_full[t ^ 1], np)) break;
+          tc_fence_after();
+          if (more) {
+            issue_qk(s_i, q0, ik);
+            commit(&slot_empty[ik % NS]);
+            if (j + 2 == n) commit(q_empty);
+          }
+          commit(more ? &s_full[t ^ 1] : &o_full[t ^ 1]);
+          if (!full(iv) || !wait(&p_full[t], np)) break;
+          tc_fence_after();
+          issue_pv(t ? o1 : o0, s_t, iv, j > 1 ? 1u : 0u);
+          commit(&slot_empty[iv % NS]);
+          commit(more ? &s_full[t] : &o_full[t]);
+        }
+        ok = true;
+      }
     }
+    // all issued tensor-core work finished before tensor memory is released
+    commit(drain);
+    mbar_wait(drain, 0, nullptr);
     __syncwarp();
-  } else if (warp >= 10) {
+  } else if (warp >= 12) {   // 10 and 11 only fill up the third warpgroup
     // -------------------------------------------------- 8-bit pages to bf16 tiles
-    if (C::kRaw) {
-      const int tid = threadIdx.x - 320;
+    if constexpr (C::kRaw) {
+      constexpr int U = D / 16;                          // 16-channel units a row
+      constexpr int RP = C::kDqWarps * 32 / U;           // rows a pass, a multiple of 8
+      constexpr int NP = 128 / RP;
+      static_assert(RP % 8 == 0 && 128 % RP == 0, "rows a pass");
+      const int tid = threadIdx.x - 384;
+      // 128-byte swizzle: 16-byte unit v of row r at v ^ (r & 7).  At D = 128 the eight
+      // threads that share a store meet both 64-column chunks, whose same units share
+      // banks: the second chunk's take the neighbouring row, which flips the unit.
+      const int c = tid % U, r0 = (tid / U) ^ (c >> 2), v = (c & 3) * 2;
+      const int src_off = r0 * D + c * 16, scale_off = C::kRawCodes + r0 * (D / kCacheGroup) + (c >> 1);
+      const int row_off = (c >> 2) * C::kChunkBytes + r0 * 128;
+      const int dst_a = row_off + ((v ^ (r0 & 7)) << 4), dst_b = row_off + (((v + 1) ^ (r0 & 7)) << 4);
       int li = 0;
       bool ok = true;
       for (int g = 0; ok; ++g) {
@@ -616,38 +955,47 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
         for (int j = sa; ok && j < sb; ++j) {
           const int key0 = (step0 + j) << 7;
           const bool partial = key0 < lo_max || key0 > hi_min - 128;
-#pragma unroll
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++li) {
-            bool w = mbar_wait(&raw_full[li % NR], (li / NR) & 1, abort_flag, wlim);
-            if (w && li >= NS) w = mbar_wait(&slot_empty[li % NS], ((li / NS) - 1) & 1, abort_flag, wlim);
-            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[li % NR], (li / NR) & 1, abort_flag, wlim))) {
+              ok = false;
+              break;
+            }
             const uint8_t* src = raw_smem + (li % NR) * C::kRawBytes;
             uint8_t* dst = slot_smem + (li % NS) * TB;
-            bool bad = false;
-#pragma unroll 4
-            for (int u = tid; u < 128 * (D / 16); u += C::kDqWarps * 32) {
-              const int r = u / (D / 16), c = u % (D / 16);
-              uint4 x = *reinterpret_cast<const uint4*>(src + r * D + c * 16), o0, o1;
-              uint32_t byte = src[C::kRawCodes + r * (D / kCacheGroup) + (c >> 1)];
-              if (kv == 1 && partial) {
-                const bool seen = key0 + r >= lo && key0 + r < hi;
-                if (!seen || byte == kCacheNanScale) {
+            uint4 x[NP];
+            uint32_t byte[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              x[i] = *reinterpret_cast<const uint4*>(src + src_off + i * RP * D);
+              byte[i] = src[scale_off + i * RP * (D / kCacheGroup)];
+            }
+            if (kv == 1 && partial) {
+              bool bad = false;
+#pragma unroll
+              for (int i = 0; i < NP; ++i) {
+                const int key = key0 + r0 + i * RP;
+                const bool seen = key >= lo && key < hi;
+                if (!seen || byte[i] == kCacheNanScale) {
                   bad = bad || seen;
-                  x = make_uint4(0u, 0u, 0u, 0u);
-                  byte = 127;
+                  x[i] = make_uint4(0u, 0u, 0u, 0u);
+                  byte[i] = 127;
                 }
               }
-              dequant16<FMT>(x, byte, o0, o1);
-              // 128-byte swizzle: 16-byte unit v of row r at v ^ (r & 7); at D = 128 the
-              // eight threads of a row meet both chunks, whose same units share banks, so
-              // the second chunk's threads store their odd unit first
-              const int v = (c & 3) * 2, chunk = c >> 2;
-              uint8_t* base = dst + chunk * C::kChunkBytes + r * 128;
-              const int first = chunk & 1;
-              *reinterpret_cast<uint4*>(base + (((v + first) ^ (r & 7)) << 4)) = first ? o1 : o0;
-              *reinterpret_cast<uint4*>(base + (((v + 1 - first) ^ (r & 7)) << 4)) = first ? o0 : o1;
+              if (bad) poison[g % kSegRing] = g + 1;
             }
-            if (bad) poison[g % kSegRing] = g + 1;
+            if (li >= NS && !__all_sync(0xffffffffu, mbar_wait(&slot_empty[li % NS], ((li / NS) - 1) & 1, abort_flag,
+                                                               wlim))) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              uint4 o0, o1;
+              dequant16<FMT>(x[i], byte[i], o0, o1);
+              *reinterpret_cast<uint4*>(dst + dst_a + i * RP * 128) = o0;
+              *reinterpret_cast<uint4*>(dst + dst_b + i * RP * 128) = o1;
+            }
             fence_async_shared();
             __syncwarp();
             if (lane == 0) {
@@ -658,275 +1006,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
         }
       }
     }
-  } else {
-    // -------------------------------------------------------------- softmax
-    const int tile = warp >> 2;
-    const int t = threadIdx.x - tile * 128;
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t col_s = 256u + 128u * tile, col_o = 128u * tile;
-    const float c2 = p.scale_log2;
-    const int rtok = t / p.group, rhead = t - rtok * p.group;
-    int ns = 0, no = 0, nml = 0, li = 0;      // s_full and o_full phases, narrow joins, K / V tiles
-    bool ok = true;
-    for (int g = 0; ok; ++g) {
-      if (!__all_sync(0xffffffffu, seg_wait(g))) break;
-      const CacheSeg& sg = segs[g % kSegRing];
-      if (sg.end) break;
-      // this thread's row: in a narrow segment both warpgroups have the same rows
-      const int tok = rtok + (sg.narrow ? 0 : tile * p.tile_tokens);
-      const bool valid = rtok < p.tile_tokens && tok < sg.it.ntok;
-      int32_t lo = 0, hi = INT32_MAX;    // rows that are not there count as seeing all: nothing to mask
-      if (valid) seen_range(p.frame, p.window, sg.it.pos0 + tok, sg.it.len, lo, hi);
-      const bool warp_rows = __any_sync(0xffffffffu, valid);
-      const int sa = sg.sa, sb = sg.sb, step0 = sg.it.step0;
-      float m_used = -INFINITY, l = 0.f;
-      for (int j = sa; j < sb; ++j, li += 2) {
-        const int32_t key0 = (step0 + j) << 7;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[tile], ns & 1, abort_flag, wlim))) { ok = false; break; }
-        ++ns;
-        tc_fence_after();
-        if (!C::kRaw && tile == 0 && seg_partial(sg, j)) {
-          // thread = key: V rows that nobody sees, or that are not finite
-          if (!__all_sync(0xffffffffu,
-                          mbar_wait(&slot_full[(li + 1) % NS], ((li + 1) / NS) & 1, abort_flag, wlim))) {
-            ok = false;
-            break;
-          }
-          uint8_t* vrow = slot_smem + ((li + 1) % NS) * TB + t * 128;
-          const bool seen = key0 + t >= sg.it.lo && key0 + t < sg.it.hi;
-          bool bad = false;
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              uint4* at = reinterpret_cast<uint4*>(vrow + c * C::kChunkBytes + u * 16);
-              uint4 y = make_uint4(0u, 0u, 0u, 0u);
-              if (seen) {
-                const uint4 x = *at;
-                y = make_uint4(finite_bf16x2(x.x), finite_bf16x2(x.y), finite_bf16x2(x.z), finite_bf16x2(x.w));
-                if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
-                bad = true;
-              }
-              *at = y;
-            }
-          if (bad) poison[g % kSegRing] = g + 1;
-          fence_async_shared();
-        }
-        if (warp_rows && seg_active(sg, tile, j)) {
-          const int32_t rl = max(lo - key0, 0), rh = min(hi - key0, 128);   // columns [rl, rh) count
-          // of each 64-column half: all lanes see all of it, or none any
-          uint32_t half_full = 0, half_none = 0;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (__all_sync(0xffffffffu, rl <= 64 * h && rh >= 64 * h + 64)) half_full |= 1u << h;
-            if (__all_sync(0xffffffffu, rl >= 64 * h + 64 || rh <= 64 * h)) half_none |= 1u << h;
-          }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if ((half_none >> h) & 1u) continue;
-            float sv[64];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t r[32];
-              tmem_ld32(taddr + lane_base + col_s + h * 64 + c * 32, r);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(r[i]);
-            }
-            tmem_wait_ld();
-            if ((half_full >> h) & 1u) {
-              float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-              for (int i = 0; i < 64; i += 8) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) m4[u] = fmax3(m4[u], sv[i + 2 * u], sv[i + 2 * u + 1]);
-              }
-              mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 64; ++i)
-                if (h * 64 + i >= rl && h * 64 + i < rh) mx = fmaxf(mx, sv[i]);
-            }
-          }
-          const float m_new = fmaxf(m_used, mx * c2);
-          const bool need = valid && m_used != -INFINITY && m_new > m_used + 8.0f;
-          if (__any_sync(0xffffffffu, need)) {
-            const float alpha = need ? ex2_approx(m_used - m_new) : 1.0f;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t r[32];
-              tmem_ld32(taddr + lane_base + col_o + c * 32, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-              tmem_st32(taddr + lane_base + col_o + c * 32, r);
-            }
-            if (need) {
-              l *= alpha;
-              m_used = m_new;
-            }
-          }
-          if (m_used == -INFINITY) m_used = m_new;
-          // a row whose logits so far are all -inf keeps 0 as its reference: every P is 0
-          const float ref = m_used == -INFINITY ? 0.f : m_used;
-          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const float2 cc = make_float2(c2, c2), mm = make_float2(-ref, -ref);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
-            if ((half_none >> h) & 1u) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) pk[i] = 0u;
-            } else {
-              float sv[64];
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t r[32];
-                tmem_ld32(taddr + lane_base + col_s + h * 64 + c * 32, r);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(r[i]);
-              }
-              tmem_wait_ld();
-              const bool all = (half_full >> h) & 1u;
-              if (!all) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                  if (h * 64 + i < rl || h * 64 + i >= rh) sv[i] = -INFINITY;
-              }
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float2 x = __ffma2_rn(make_float2(sv[2 * i], sv[2 * i + 1]), cc, mm);
-                const float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                acc[i & 3] = __fadd2_rn(acc[i & 3], pe);
-                pk[i] = pack_bf16x2(pe.x, pe.y);
-              }
-            }
-            tmem_st32(taddr + lane_base + col_s + h * 32, pk);
-          }
-          const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-          l += a.x + a.y;
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[tile]);
-      }
-      if (!ok) break;
-      // the last product into this tile's O
-      bool have = false, have1 = false;
-      if (sb > sa) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&o_full[tile], no & 1, abort_flag, wlim))) { ok = false; break; }
-        ++no;
-        tc_fence_after();
-        have = sg.narrow ? sb - sa > tile : max(sa, sg.act_a[tile]) < min(sb, sg.act_b[tile]);
-      }
-      float w0 = 1.f, w1 = 0.f;
-      if (sg.narrow && sb > sa) {
-        if (tile == 1) {
-          ml[t] = make_float2(m_used, l);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ml_full);
-          if (!__all_sync(0xffffffffu, mbar_wait(ml_done, nml & 1, abort_flag, wlim))) { ok = false; break; }
-        } else {
-          if (!__all_sync(0xffffffffu, mbar_wait(ml_full, nml & 1, abort_flag, wlim))) { ok = false; break; }
-          tc_fence_after();
-          if (sb - sa > 1) {
-            have1 = true;
-            const float2 b = ml[t];
-            const float m = fmaxf(m_used, b.x);
-            w0 = m_used == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_approx(m_used - m);
-            w1 = b.x == -INFINITY ? (b.y == 0.f ? 0.f : 1.f) : ex2_approx(b.x - m);
-            l = l * w0 + b.y * w1;
-            m_used = m;
-          }
-        }
-        ++nml;
-      }
-      if (warp_rows && !(sg.narrow && tile == 1)) {
-        const bool poisoned = poison[g % kSegRing] == g + 1;
-        const bool part = sg.part >= 0;
-        const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-        const int64_t token = sg.it.tok0 + tok;
-        const int qhead = sg.head * p.group + rhead;
-        __nv_bfloat16* orow = p.o + token * p.o_token + qhead * p.o_head;
-        const int64_t prow = part ? (2 * static_cast<int64_t>(blockIdx.x) + sg.part) * C::kRows +
-                                        (sg.narrow ? 0 : tile * 128) + t
-                                  : 0;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float x[32];
-          {
-            uint32_t r[32];
-            if (have) {
-              tmem_ld32(taddr + lane_base + col_o + c * 32, r);
-              tmem_wait_ld();
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = have && w0 != 0.f ? __uint_as_float(r[i]) * w0 : 0.f;
-            if (have1) {
-              tmem_ld32(taddr + lane_base + 128u + c * 32, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (w1 != 0.f) x[i] = fmaf(__uint_as_float(r[i]), w1, x[i]);
-            }
-          }
-          if (poisoned && valid) {
-            for (int j = sa; j < sb; ++j) {
-              if (!seg_partial(sg, j)) continue;
-              const int32_t key0 = (step0 + j) << 7;
-              for (int32_t key = max(lo, key0); key < min(hi, key0 + 128); ++key) {
-                const int64_t at = cache_row(p.c, p.s, sg.it.seq, key);
-                if (at < 0) continue;
-                const int64_t row = at + (static_cast<int64_t>(sg.head) << p.c.page_shift);
-                if (C::kRaw) {
-                  if (p.c.v_scale[row * (D / kCacheGroup) + c] == kCacheNanScale) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __int_as_float(0x7fffffff);
-                  }
-                } else {
-                  const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.c.v) + row * D;
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) {
-                    const float f = __bfloat162float(v[c * 32 + i]);
-                    if (!isfinite(f)) x[i] += f;
-                  }
-                }
-              }
-            }
-          }
-          if (valid) {
-            if (part) {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                dst[i] = make_uint4(pack_bf16x2(x[8 * i] * inv, x[8 * i + 1] * inv),
-                                    pack_bf16x2(x[8 * i + 2] * inv, x[8 * i + 3] * inv),
-                                    pack_bf16x2(x[8 * i + 4] * inv, x[8 * i + 5] * inv),
-                                    pack_bf16x2(x[8 * i + 6] * inv, x[8 * i + 7] * inv));
-            }
-          }
-        }
-        if (valid) {
-          if (part)
-            p.part_ml[prow] = make_float2(m_used, l);
-          else
-            p.lse[static_cast<int64_t>(qhead) * p.s.num_tokens + token] =
-                l == 0.f ? -INFINITY : m_used * 0.69314718055994531f + __logf(l);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (sg.narrow && sb > sa && tile == 0) mbar_arrive(ml_done);
-        mbar_arrive(&seg_empty[g % kSegRing]);
-      }
-    }
+  }
   }
 
   tc_fence_before();

@@ -107,38 +107,51 @@ __device__ __forceinline__ uint32_t pow2_bf16x2(int e) {
   return b | (b << 16);
 }
 
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+
 // Four stored bytes -> four bf16 numbers, before their scale.  e4m3: the seven
 // low bits moved to bf16's exponent and mantissa are the value times 2^-120
-// (subnormals included).  int8: 128 + the seven low bits is a bf16 number, and
-// so is the 128 or 256 to take from it.
+// (subnormals included); one permute puts each byte in a high half, with the first
+// one's sign spread over the byte above it (selector bit 3), so that one
+// arithmetic shift by 4 carries both signs along and a mask clears the rest.
+// int8: 128 + the seven low bits is a bf16 number, and so is the 128 or 256 to
+// take from it.
 template <int FMT>
 __device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if (FMT == kCacheE4m3) {
-    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);   // byte in the high half
-    lo = (a & 0x80008000u) | ((a & 0x7f007f00u) >> 4);
-    hi = (b & 0x80008000u) | ((b & 0x7f007f00u) >> 4);
+    lo = static_cast<uint32_t>(static_cast<int32_t>(prmt(w, 0u, 0x1804u)) >> 4) & 0x87f087f0u;
+    hi = static_cast<uint32_t>(static_cast<int32_t>(prmt(w, 0u, 0x3a24u)) >> 4) & 0x87f087f0u;
   } else {
-    const uint32_t a = __byte_perm(w, 0x43434343u, 0x4140), b = __byte_perm(w, 0x43434343u, 0x4342);
+    const uint32_t a = prmt(w, 0x43434343u, 0x4140u), b = prmt(w, 0x43434343u, 0x4342u);
     lo = sub_bf16x2(a & 0xff7fff7fu, a & 0xff80ff80u);
     hi = sub_bf16x2(b & 0xff7fff7fu, b & 0xff80ff80u);
   }
 }
 
-// Factors of a scale byte for what unpack4 gives: the second is 1 unless the
-// first would leave bf16's range (scales over 2^7 of e4m3 pages).
+// Factors of a scale byte for what unpack4 gives.  The first alone does (and the
+// second is 1) but for scales over 2^7 of e4m3 pages, whose factor would leave
+// bf16's range.
+constexpr uint32_t kBf16One = 0x3f803f80u;
+
 template <int FMT>
 __device__ __forceinline__ void scale_factors(uint32_t byte, uint32_t& f1, uint32_t& f2) {
-  f2 = 0x3f803f80u;
-  if (byte == kCacheNanScale) {
-    f1 = 0x7fc07fc0u;
-    return;
+  constexpr uint32_t kBias = FMT == kCacheE4m3 ? 120u : 0u;   // unpack4 gives e4m3 times 2^-120
+  f1 = (byte + kBias) * 0x00800080u;                          // the exponent field, twice
+  f2 = kBf16One;
+  if (byte + kBias - 1u > 253u) {
+    if (byte == kCacheNanScale) {
+      f1 = 0x7fc07fc0u;
+    } else if (byte == 0u) {       // int8: 2^-127, a subnormal
+      f1 = 0x00400040u;
+    } else {
+      f1 = 0x7f007f00u;            // 2^127
+      f2 = pow2_bf16x2(static_cast<int>(byte + kBias) - 254);
+    }
   }
-  int e = static_cast<int>(byte) - 127 + (FMT == kCacheE4m3 ? 120 : 0);
-  if (e > 127) {
-    f2 = pow2_bf16x2(e - 127);
-    e = 127;
-  }
-  f1 = pow2_bf16x2(e);
 }
 
 // 16 stored bytes under one scale -> 16 bf16 numbers.
@@ -152,7 +165,7 @@ __device__ __forceinline__ void dequant16(const uint4& w, uint32_t byte, uint4& 
   unpack4<FMT>(w.w, o1.z, o1.w);
   o0.x = mul_bf16x2(o0.x, f1); o0.y = mul_bf16x2(o0.y, f1); o0.z = mul_bf16x2(o0.z, f1); o0.w = mul_bf16x2(o0.w, f1);
   o1.x = mul_bf16x2(o1.x, f1); o1.y = mul_bf16x2(o1.y, f1); o1.z = mul_bf16x2(o1.z, f1); o1.w = mul_bf16x2(o1.w, f1);
-  if (FMT == kCacheE4m3 && f2 != 0x3f803f80u) {
+  if (FMT == kCacheE4m3 && f2 != kBf16One) {
     o0.x = mul_bf16x2(o0.x, f2); o0.y = mul_bf16x2(o0.y, f2); o0.z = mul_bf16x2(o0.z, f2); o0.w = mul_bf16x2(o0.w, f2);
     o1.x = mul_bf16x2(o1.x, f2); o1.y = mul_bf16x2(o1.y, f2); o1.z = mul_bf16x2(o1.z, f2); o1.w = mul_bf16x2(o1.w, f2);
   }
