@@ -90,7 +90,7 @@ struct CacheAttnParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;                    // [heads, num_tokens]
-  int64_t o_token, o_head;       // strides in elements
+  int64_t q_token, q_head, o_token, o_head;   // strides in elements
   int32_t group;                 // query heads of a K / V head
   int32_t tile_tokens;           // tokens of a 128-row tile: 128 / group
   int32_t frame, window;

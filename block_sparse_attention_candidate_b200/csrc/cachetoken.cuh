@@ -1,0 +1,453 @@
+// Attention of single tokens (16 rows at most of a sequence and K / V head) over
+// 8-bit pages: the same mathematics and schedule as cacheattn.cuh, for calls whose
+// time is the reading of the cache.
+//
+// The tensor-core tiles of cacheattn.cuh want bf16 operands in shared memory.  For
+// few rows that detour is the bound: 64 KB written and 96 KB read again by the
+// products for every 33 KB of 128 keys.  Here a warp turns the stored bytes into
+// register fragments of a 16 x 8 x 16 product (warp_mma.cuh) and nothing goes
+// back: shared memory holds the bytes alone, once written and once read.
+// Measured (3 sequences of 131,072 keys, 8 K / V heads, e4m3): see cache_token_kernel.
+//
+// Fragments without a shuffle.  The product sums over channels (Q K^T) or keys
+// (P V) in any order and its columns may be any keys or channels, so they are named
+// to suit 16-byte reads (thread 4 g + t of the warp):
+//   Q K^T  column g of key tile n is key 8 n + 4 (g & 1) + g / 2; thread t has the
+//          16 channels of chunk t (and t + 4): word kk of it is step kk's operand;
+//   P V    the sums over keys run over 16 keys in the order that leaves each
+//          thread's S where P's operand wants it: keys t, 4 + t, 8 + t, 12 + t;
+//          column g of channel tile j is channel 16 c(g) + j (8 c(g) + j at D = 64),
+//          byte j of what the thread read.
+// The bytes lie in shared memory so that the threads served together meet
+// different banks: 16-byte chunk c of row r at c ^ (r & 7) (D = 128).  At D = 64, K's
+// row r takes place 2 (r & 3) + r / 4 of its eight and V's chunk c is at
+// c ^ ((r / 2) & 3).
+//
+// A CTA has six warps and an SM two CTAs; a segment's 16-key blocks go to the warps
+// in turn, each warp with a ring of its own, filled by cp.async, and its own max, sum
+// and O.  At the end of a segment the six are joined in shared memory while the
+// SM's other CTA reads on.
+#pragma once
+
+#include "cacheattn.cuh"
+#include "warp_mma.cuh"
+
+namespace dynrad {
+
+constexpr int kTokenRows = 16;       // rows of an item
+constexpr int kTokenWarps = 6;
+constexpr int kTokenThreads = kTokenWarps * 32;
+constexpr int kTokenCtasPerSm = 2;
+constexpr int kTokenKeys = 16;       // keys of a block
+
+template <int D>
+struct CacheTokenCfg {
+  static constexpr int kCodes = kTokenKeys * D;
+  static constexpr int kScales = kTokenKeys * (D / kCacheGroup);
+  static constexpr int kStageBytes = 2 * (kCodes + kScales);    // K, V, K's scales, V's scales
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kOut = kTokenRows * D * 4;               // a warp's O, over its ring
+  static constexpr int kSmem = kTokenWarps * kRingBytes + 2048;
+  static_assert(kOut <= kRingBytes, "O over the ring");
+  static_assert(kTokenCtasPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool fill) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(fill ? 4 : 0) : "memory");
+}
+
+// Byte k of a (in the low half) and of b -> a bf16 pair, before their scales
+// (unpack4 with the bytes of two words).
+template <int FMT, int K>
+__device__ __forceinline__ uint32_t unpack_pair(uint32_t a, uint32_t b) {
+  constexpr uint32_t kSel = ((4u + K) << 12) | ((8u | K) << 8) | (K << 4) | K;
+  if (FMT == kCacheE4m3) return static_cast<uint32_t>(static_cast<int32_t>(prmt(a, b, kSel)) >> 4) & 0x87f087f0u;
+  const uint32_t w = prmt(a, b, ((4u + K) << 8) | (4u + K) << 12 | (K << 4) | K);
+  return sub_bf16x2((w & 0x007f007fu) | 0x43004300u, (w & 0x00800080u) | 0x43004300u);
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_kernel(const CacheAttnParams p) {
+  using C = CacheTokenCfg<D>;
+  constexpr int KW = D == 128 ? 2 : 1;       // 16-byte chunks of a key that a thread reads
+  constexpr int NJ = D / 8;                  // channel tiles
+  constexpr int VB = D / 8;                  // bytes of a V row that a thread reads: 16 or 8
+  extern __shared__ __align__(128) uint8_t token_smem[];
+  uint8_t* ctrl = token_smem + kTokenWarps * C::kRingBytes;
+  CacheRun* run = reinterpret_cast<CacheRun*>(ctrl);                       // 24 bytes
+  volatile int* poison = reinterpret_cast<volatile int*>(ctrl + 32);
+  CacheSeg* seg_s = reinterpret_cast<CacheSeg*>(ctrl + 64);
+  float2* ml = reinterpret_cast<float2*>(ctrl + 256);                      // [warp][row]
+  static_assert(64 + sizeof(CacheSeg) <= 256 && 256 + kTokenWarps * kTokenRows * 8 <= 2048, "control block");
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int item_tokens = p.tile_tokens;
+  const int ps = p.c.page_shift;
+  int place, head;
+  int64_t off = 0, left = 1;
+  if (p.split) {
+    plan_run<kTokenThreads>(p, item_tokens, reinterpret_cast<int32_t*>(token_smem), reinterpret_cast<int64_t*>(ml), run);
+    left = run->left;
+    off = left > 0 ? run->off : 0;
+    head = left > 0 ? run->head : 0;
+    place = left > 0 ? run->place : 0;
+    if (threadIdx.x < 2) p.part_desc[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, kPartNone, 0);
+  } else {
+    head = blockIdx.y;
+    place = p.slots - 1 - static_cast<int>(blockIdx.x);
+  }
+
+  uint8_t* ring = token_smem + warp * C::kRingBytes;
+  const uint32_t ring_u = smem_u32(ring);
+  // where this thread reads: chunk t of its key of the first key tile; its part of V row t
+  const int krow = (g & 1) * 4 + (g >> 1);
+  const int k_off = D == 128 ? krow * 128 + ((t ^ krow) << 4) : g * 64 + (t << 4);
+  const int vc = D == 128 ? krow : (g & 1) | ((g & 2) << 1) | ((g & 4) >> 1);   // c(g)
+  // of V row r = t + 4 i (r & 7 = t + 4 (i & 1))
+  auto v_off = [&](int i) -> int {
+    const int r = t + 4 * i;
+    return D == 128 ? r * 128 + ((vc ^ (r & 7)) << 4) : r * 64 + (((vc >> 1) ^ ((r >> 1) & 3)) << 4) + (vc & 1) * 8;
+  };
+  const int v_group = vc * VB / kCacheGroup;
+
+  while (left > 0) {
+    // the next segment, found by one warp
+    __syncthreads();
+    if (warp == 0) {
+      CacheSeg sg;
+      for (;;) {
+        sg.it = find_item(p, item_tokens, place);
+        const int32_t units = item_units(sg.it);
+        sg.head = head;
+        sg.sa = 0;
+        sg.sb = sg.it.steps;
+        sg.part = -1;
+        if (p.split) {
+          const int64_t take = min(left, static_cast<int64_t>(units) - off);
+          if (units > 0) {
+            sg.sa = static_cast<int32_t>(max(off - kCacheItemCost, static_cast<int64_t>(0)));
+            sg.sb = static_cast<int32_t>(max(off + take - kCacheItemCost, static_cast<int64_t>(0)));
+            left -= take;
+          }
+          off = 0;
+        } else {
+          left = 0;
+        }
+        const int at = place;
+        if (++place == p.slots) {
+          place = 0;
+          if (++head == p.c.heads) left = 0;
+        }
+        const bool use = units > 0 && (sg.sb > sg.sa || sg.it.steps == 0);
+        if (use && !(sg.sa == 0 && sg.sb == sg.it.steps)) {
+          sg.part = sg.sa > 0 ? 0 : 1;
+          if (lane == 0)
+            p.part_desc[2 * blockIdx.x + sg.part] =
+                make_int4(at, sg.head, sg.sb == sg.it.steps ? kPartLast : kPartOpen, 0);
+        }
+        sg.end = use ? 0 : 1;
+        if (use || left <= 0) break;
+      }
+      if (lane == 0) {
+        sg.narrow = left > 0;        // more segments follow
+        *seg_s = sg;
+        *poison = 0;
+      }
+    }
+    __syncthreads();
+    const CacheItem it = seg_s->it;
+    const int sa = seg_s->sa, sb = seg_s->sb, part = seg_s->part, kvh = seg_s->head;
+    if (seg_s->end) break;
+    left = seg_s->narrow ? max(left, static_cast<int64_t>(1)) : 0;   // warp 0 keeps the count
+
+    const int rows = it.ntok * p.group;
+    // this thread's rows g and g + 8: what they see, and Q's operands
+    int32_t rlo[2], rhi[2];
+    uint32_t q[2][KW * 8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i, tok = r / p.group;
+      rlo[i] = 0;
+      rhi[i] = INT32_MAX;     // rows that are not there count as seeing all
+#pragma unroll
+      for (int w = 0; w < KW * 8; ++w) q[i][w] = 0u;
+      if (r < rows) {
+        seen_range(p.frame, p.window, it.pos0 + tok, it.len, rlo[i], rhi[i]);
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (it.tok0 + tok) * p.q_token +
+                                                          (kvh * p.group + r - tok * p.group) * p.q_head);
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint4 x = src[(t + 4 * w) * 2 + u];
+            q[i][w * 8 + u * 4] = x.x;
+            q[i][w * 8 + u * 4 + 1] = x.y;
+            q[i][w * 8 + u * 4 + 2] = x.z;
+            q[i][w * 8 + u * 4 + 3] = x.w;
+          }
+      }
+    }
+    float o[NJ][4];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) o[j][u] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    // 16-key blocks [b0, b1) of the segment; this warp has b0 + warp, + 6, ..
+    const int64_t ka = max(static_cast<int64_t>(it.lo), static_cast<int64_t>(it.step0 + sa) << 7);
+    const int64_t kb = min(static_cast<int64_t>(it.hi), static_cast<int64_t>(it.step0 + sb) << 7);
+    const int b0 = static_cast<int>(ka >> 4), b1 = sb > sa ? static_cast<int>((kb + 15) >> 4) : b0;
+    const int32_t* table = p.s.page_table + static_cast<int64_t>(it.seq) * p.s.table_stride;
+    auto page_of = [&](int b) -> int32_t { return b < b1 ? table[b >> (ps - 4)] : 0; };
+    auto load = [&](int b, int32_t pg, int stage) {
+      if (b < b1) {
+        const bool good = pg >= 0 && pg < p.c.num_pages;
+        if (!good && lane == 0) record_error(DYNRAD_ERR_DEVICE);
+        // a page outside the pool is filled with zeros
+        const int64_t row = good ? (((static_cast<int64_t>(pg) * p.c.heads + kvh) << ps) + ((b << 4) & ((1 << ps) - 1))) : 0;
+        const uint8_t* kc = p.c.k + row * D;
+        const uint8_t* vcodes = p.c.v + row * D;
+        const uint32_t dst = ring_u + stage * C::kStageBytes;
+#pragma unroll
+        for (int i = 0; i < C::kCodes / 512; ++i) {
+          const int u = lane + 32 * i, r = u / (D / 16), c = u % (D / 16);
+          const int kr = D == 128 ? r : (r & 8) + (r & 3) * 2 + ((r >> 2) & 1);
+          const int kcx = D == 128 ? c ^ (r & 7) : c, vcx = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+          cp_async16(dst + kr * D + kcx * 16, kc + u * 16, good);
+          cp_async16(dst + C::kCodes + r * D + vcx * 16, vcodes + u * 16, good);
+        }
+        constexpr int W = C::kScales / 4;     // 16 or 8 words each
+        if (lane < 2 * W) {
+          const uint8_t* sc = (lane < W ? p.c.k_scale : p.c.v_scale) + row * (D / kCacheGroup) + (lane % W) * 4;
+          cp_async4(dst + 2 * C::kCodes + lane * 4, sc, good);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int b = b0 + warp;
+    {
+      int32_t pg[C::kStages];
+#pragma unroll
+      for (int s = 0; s < C::kStages; ++s) pg[s] = page_of(b + s * kTokenWarps);
+#pragma unroll
+      for (int s = 0; s < C::kStages; ++s) load(b + s * kTokenWarps, pg[s], s);
+    }
+    int32_t next_page = page_of(b + C::kStages * kTokenWarps);
+    int stage = 0;
+#pragma unroll 1
+    for (; b < b1; b += kTokenWarps) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
+      __syncwarp();
+      const uint8_t* st = ring + stage * C::kStageBytes;
+      const uint8_t* ksc = st + 2 * C::kCodes;
+      const uint8_t* vsc = ksc + C::kScales;
+      const int key0 = b << 4;
+      const bool partial = key0 < it.lo_max || key0 > it.hi_min - 16;
+      // S = Q K^T: two tiles of eight keys
+      float s[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[n][u] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const uint4 x = *reinterpret_cast<const uint4*>(st + n * 8 * D + (w == 0 ? k_off : k_off ^ 64));
+          const uint32_t byte = ksc[(n * 8 + krow) * (D / kCacheGroup) + w * 2 + (t >> 1)];
+          uint32_t f1, f2, a[4], c[4];
+          scale_factors<FMT>(byte, f1, f2);
+          unpack4<FMT>(x.x, a[0], c[0]);
+          unpack4<FMT>(x.y, a[1], c[1]);
+          unpack4<FMT>(x.z, a[2], c[2]);
+          unpack4<FMT>(x.w, a[3], c[3]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            a[u] = mul_bf16x2(a[u], f1);
+            c[u] = mul_bf16x2(c[u], f1);
+          }
+          if (FMT == kCacheE4m3 && __any_sync(0xffffffffu, f2 != kBf16One)) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              a[u] = mul_bf16x2(a[u], f2);
+              c[u] = mul_bf16x2(c[u], f2);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            mma_16816(s[n], q[0][w * 8 + 2 * u], q[1][w * 8 + 2 * u], q[0][w * 8 + 2 * u + 1], q[1][w * 8 + 2 * u + 1],
+                      a[u], c[u]);
+        }
+      }
+      if (partial) {     // s[n][2 i + e]: row g + 8 i, key 8 n + 4 e + t
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int key = key0 + 8 * n + 4 * (u & 1) + t;
+            if (key < rlo[u >> 1] || key >= rhi[u >> 1]) s[n][u] = -INFINITY;
+          }
+      }
+      uint32_t pf[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = fmaxf(fmax3(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]), s[1][2 * i + 1]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float m_new = fmaxf(m[i], mx * p.scale_log2);
+        const bool need = m_new > m[i] + 8.0f;     // the first seen key's block too: m = -inf
+        if (__any_sync(0xffffffffu, need)) {
+          const float alpha = need ? ex2_approx(m[i] - m_new) : 1.0f;
+          if (need) m[i] = m_new;
+          l[i] *= alpha;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            o[j][2 * i] *= alpha;
+            o[j][2 * i + 1] *= alpha;
+          }
+        }
+        const float ref = m[i] == -INFINITY ? 0.f : m[i];
+        float e[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) e[u] = ex2_approx(fmaf(s[u >> 1][2 * i + (u & 1)], p.scale_log2, -ref));
+        l[i] += (e[0] + e[1]) + (e[2] + e[3]);
+        pf[i] = pack_bf16x2(e[0], e[1]);
+        pf[2 + i] = pack_bf16x2(e[2], e[3]);
+      }
+      // O += P V: V rows t, 4 + t (first operand register), 8 + t, 12 + t (second)
+      uint32_t x[4][VB / 4], byte[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* src = st + C::kCodes + v_off(i);
+        if (D == 128) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src);
+          x[i][0] = v.x;
+          x[i][1] = v.y;
+          x[i][VB / 4 - 2] = v.z;
+          x[i][VB / 4 - 1] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(src);
+          x[i][0] = v.x;
+          x[i][1] = v.y;
+        }
+        byte[i] = vsc[(t + 4 * i) * (D / kCacheGroup) + v_group];
+      }
+      if (partial) {     // what no row sees, and NaN, stay out of the product (cacheattn.cuh)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = key0 + t + 4 * i;
+          const bool seen = key >= it.lo && key < it.hi;
+          if (!seen || byte[i] == kCacheNanScale) {
+            if (seen) *poison = 1;
+            byte[i] = 127;
+#pragma unroll
+            for (int w = 0; w < VB / 4; ++w) x[i][w] = 0u;
+          }
+        }
+      }
+      uint32_t f1[4], f2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) scale_factors<FMT>(byte[i], f1[i], f2[i]);
+      const uint32_t fa = prmt(f1[0], f1[1], 0x5410u), fb = prmt(f1[2], f1[3], 0x5410u);
+      const bool big = FMT == kCacheE4m3 &&
+          __any_sync(0xffffffffu, f2[0] != kBf16One || f2[1] != kBf16One || f2[2] != kBf16One || f2[3] != kBf16One);
+      const uint32_t ga = prmt(f2[0], f2[1], 0x5410u), gb = prmt(f2[2], f2[3], 0x5410u);
+      auto tile = [&](int j, uint32_t a, uint32_t c) {
+        a = mul_bf16x2(a, fa);
+        c = mul_bf16x2(c, fb);
+        if (big) {
+          a = mul_bf16x2(a, ga);
+          c = mul_bf16x2(c, gb);
+        }
+        mma_16816(o[j], pf[0], pf[1], pf[2], pf[3], a, c);
+      };
+#pragma unroll
+      for (int w = 0; w < VB / 4; ++w) {
+        tile(4 * w, unpack_pair<FMT, 0>(x[0][w], x[1][w]), unpack_pair<FMT, 0>(x[2][w], x[3][w]));
+        tile(4 * w + 1, unpack_pair<FMT, 1>(x[0][w], x[1][w]), unpack_pair<FMT, 1>(x[2][w], x[3][w]));
+        tile(4 * w + 2, unpack_pair<FMT, 2>(x[0][w], x[1][w]), unpack_pair<FMT, 2>(x[2][w], x[3][w]));
+        tile(4 * w + 3, unpack_pair<FMT, 3>(x[0][w], x[1][w]), unpack_pair<FMT, 3>(x[2][w], x[3][w]));
+      }
+      __syncwarp();      // every lane has read the stage
+      load(b + C::kStages * kTokenWarps, next_page, stage);
+      next_page = page_of(b + (C::kStages + 1) * kTokenWarps);
+      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+
+    // join the warps: O over their rings
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      const int r = g + 8 * i;
+      if (t == 0) ml[warp * kTokenRows + r] = make_float2(m[i], l[i]);
+      // columns 2 t and 2 t + 1 of tile j: channels base + j of two runs
+      float* dst = reinterpret_cast<float*>(ring) + r * D;
+      const int c0 = D == 128 ? 16 * t : 8 * ((((2 * t) & 2) << 1) | (((2 * t) & 4) >> 1));
+      const int c1 = D == 128 ? 64 + 16 * t : c0 + 8;
+#pragma unroll
+      for (int j = 0; j < NJ; j += 4) {
+        *reinterpret_cast<float4*>(dst + c0 + j) =
+            make_float4(o[j][2 * i], o[j + 1][2 * i], o[j + 2][2 * i], o[j + 3][2 * i]);
+        *reinterpret_cast<float4*>(dst + c1 + j) =
+            make_float4(o[j][2 * i + 1], o[j + 1][2 * i + 1], o[j + 2][2 * i + 1], o[j + 3][2 * i + 1]);
+      }
+    }
+    __syncthreads();
+    const bool poisoned = *poison != 0;
+    for (int u = threadIdx.x; u < rows * (D / 4); u += kTokenThreads) {
+      const int r = u / (D / 4), c = u % (D / 4);
+      float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kTokenWarps; ++w) mm = fmaxf(mm, ml[w * kTokenRows + r].x);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kTokenWarps; ++w) {
+        const float2 x = ml[w * kTokenRows + r];
+        const float f = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2_approx(x.x - mm);
+        if (f == 0.f) continue;
+        const float4 v = reinterpret_cast<const float4*>(token_smem + w * C::kRingBytes + r * (D * 4))[c];
+        ll = fmaf(x.y, f, ll);
+        a.x = fmaf(v.x, f, a.x);
+        a.y = fmaf(v.y, f, a.y);
+        a.z = fmaf(v.z, f, a.z);
+        a.w = fmaf(v.w, f, a.w);
+      }
+      const int tok = r / p.group, qhead = kvh * p.group + r - tok * p.group;
+      if (poisoned) {
+        int32_t lo, hi;
+        seen_range(p.frame, p.window, it.pos0 + tok, it.len, lo, hi);
+        const int first = max(lo, static_cast<int>(ka)), last = min(static_cast<int64_t>(hi), kb);
+        for (int key = first; key < last; ++key) {
+          const int k0 = key & ~15;
+          if (!(k0 < it.lo_max || k0 > it.hi_min - 16)) continue;
+          const int64_t at = cache_row(p.c, p.s, it.seq, key);
+          if (at >= 0 && p.c.v_scale[(at + (static_cast<int64_t>(kvh) << ps)) * (D / kCacheGroup) + c * 4 / kCacheGroup] ==
+                             kCacheNanScale)
+            a.x = a.y = a.z = a.w = __int_as_float(0x7fffffff);
+        }
+      }
+      const int64_t token = it.tok0 + tok;
+      if (part >= 0) {
+        const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + part) * kTokenRows + r;
+        reinterpret_cast<float4*>(p.part_o + prow * D)[c] = a;
+        if (c == 0) p.part_ml[prow] = make_float2(mm, ll);
+      } else {
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        *reinterpret_cast<uint2*>(p.o + token * p.o_token + qhead * p.o_head + c * 4) =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        if (c == 0)
+          p.lse[static_cast<int64_t>(qhead) * p.s.num_tokens + token] =
+              ll == 0.f ? -INFINITY : mm * 0.69314718055994531f + __logf(ll);
+      }
+    }
+  }
+}
+
+}  // namespace dynrad

@@ -16,6 +16,7 @@
 
 #include "attention.cuh"
 #include "cacheattn.cuh"
+#include "cachetoken.cuh"
 #include "candidates.cuh"
 #include "common.cuh"
 #include "backward.cuh"
@@ -1226,7 +1227,8 @@ namespace {
 // How a call of the cache's attention is laid out on the GPU (cacheattn.cuh).
 struct CachePlan {
   int32_t group, tile_tokens, tiles, item_tokens, slots;
-  bool split;
+  int32_t part_rows, ctas_per_sm;
+  bool token, split;   // token: cachetoken.cuh's kernel
   size_t part_ml, part_desc, total;
 };
 
@@ -1237,9 +1239,16 @@ int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, i
   pl->group = heads / c->heads;
   if (pl->group > 128) return DYNRAD_ERR_UNSUPPORTED;
   pl->tile_tokens = 128 / pl->group;
+  // 8-bit pages and sequences of 16 rows or fewer on average: the kernel that reads
+  // them once (TOKEN_FIGURES)
+  pl->token = c->format != DYNRAD_CACHE_BF16 && pl->group <= kTokenRows &&
+              static_cast<int64_t>(num_tokens) <= static_cast<int64_t>(num_seqs) * (kTokenRows / pl->group);
+  if (pl->token) pl->tile_tokens = kTokenRows / pl->group;
   // one tile an item where the sequences' tokens fill no more on average
   pl->tiles = static_cast<int64_t>(num_tokens) <= static_cast<int64_t>(num_seqs) * pl->tile_tokens ? 1 : 2;
   pl->item_tokens = pl->tiles * pl->tile_tokens;
+  pl->part_rows = pl->token ? kTokenRows : 128 * pl->tiles;
+  pl->ctas_per_sm = pl->token ? kTokenCtasPerSm : 1;
   const int64_t slots = static_cast<int64_t>(num_tokens) / pl->item_tokens + num_seqs;
   if (slots > INT32_MAX || c->heads > 65535) return DYNRAD_ERR_UNSUPPORTED;
   pl->slots = static_cast<int32_t>(slots);
@@ -1249,10 +1258,10 @@ int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, i
   const bool many = slots * c->heads >= 8 * kCacheMaxCtas &&
                     static_cast<int64_t>(num_tokens) >= static_cast<int64_t>(num_seqs) * pl->item_tokens;
   pl->split = slots <= kCacheMaxPlan && !many;
-  const size_t rows = static_cast<size_t>(2) * kCacheMaxCtas * 128 * pl->tiles;
+  const size_t ctas = static_cast<size_t>(kCacheMaxCtas) * pl->ctas_per_sm, rows = 2 * ctas * pl->part_rows;
   pl->part_ml = pl->split ? align256(rows * c->dim * 4) : 0;
   pl->part_desc = pl->split ? align256(pl->part_ml + rows * 8) : 0;
-  pl->total = pl->split ? align256(pl->part_desc + 2 * kCacheMaxCtas * 16) : 256;
+  pl->total = pl->split ? align256(pl->part_desc + 2 * ctas * 16) : 256;
   return DYNRAD_OK;
 }
 
@@ -1296,6 +1305,17 @@ int launch_cache_attn(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
   return launch_status();
 }
 
+template <int D, int FMT>
+int launch_cache_token(const CacheAttnParams& p, int ctas, cudaStream_t st) {
+  using C = CacheTokenCfg<D>;
+  static OptInTable optin;   // per instantiation, per device
+  const int rc = smem_optin(optin, reinterpret_cast<const void*>(cache_token_kernel<D, FMT>), C::kSmem);
+  if (rc != DYNRAD_OK) return rc;
+  const dim3 grid = p.split ? dim3(ctas) : dim3(p.slots, p.c.heads);
+  cache_token_kernel<D, FMT><<<grid, kTokenThreads, C::kSmem, st>>>(p);
+  return launch_status();
+}
+
 template <int D>
 int launch_cache_join(const CacheAttnParams& p, const CachePlan& pl, int ctas, cudaStream_t st) {
   // the launch overlaps the end of the attention; the kernel waits for all of it
@@ -1310,7 +1330,7 @@ int launch_cache_join(const CacheAttnParams& p, const CachePlan& pl, int ctas, c
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, p, pl.item_tokens, 128 * pl.tiles, ctas) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, p, pl.item_tokens, pl.part_rows, ctas) != cudaSuccess)
     return DYNRAD_ERR_CUDA;
   return launch_status();
 }
@@ -1345,6 +1365,9 @@ extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs
   if (workspace_bytes < pl.total) return DYNRAD_ERR_CAPACITY;
   const float sc = scale == 0.0f ? 1.0f / std::sqrt(static_cast<float>(cache->dim)) : scale;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_token = q_token_stride;
+  p.q_head = q_head_stride;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.o_token = o_token_stride;
@@ -1366,21 +1389,29 @@ extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return DYNRAD_ERR_CUDA;
-  const int ctas = std::min(sms, kCacheMaxCtas);
-  CUtensorMap mq = {}, mk = {}, mv = {};
-  const int64_t any = cache->dim;   // stride of an axis of length one: any that the map takes
-  if (!encode_cache_q(&mq, q, cache->dim, heads, p.s.num_tokens, heads > 1 ? q_head_stride : any,
-                      p.s.num_tokens > 1 ? q_token_stride : any, pl.group, pl.tile_tokens))
-    return DYNRAD_ERR_CUDA;
-  if (cache->format == DYNRAD_CACHE_BF16 &&
-      (!encode_pages(&mk, cache->k, cache) || !encode_pages(&mv, cache->v, cache)))
-    return DYNRAD_ERR_CUDA;
+  const int ctas = std::min(sms, kCacheMaxCtas) * pl.ctas_per_sm;
   cudaStream_t st = as_stream(stream);
+  if (pl.token) {
+    const bool e4m3 = cache->format == DYNRAD_CACHE_E4M3;
+    if (cache->dim == 128)
+      rc = e4m3 ? launch_cache_token<128, kCacheE4m3>(p, ctas, st) : launch_cache_token<128, kCacheInt8>(p, ctas, st);
+    else
+      rc = e4m3 ? launch_cache_token<64, kCacheE4m3>(p, ctas, st) : launch_cache_token<64, kCacheInt8>(p, ctas, st);
+  } else {
+    CUtensorMap mq = {}, mk = {}, mv = {};
+    const int64_t any = cache->dim;   // stride of an axis of length one: any that the map takes
+    if (!encode_cache_q(&mq, q, cache->dim, heads, p.s.num_tokens, heads > 1 ? q_head_stride : any,
+                        p.s.num_tokens > 1 ? q_token_stride : any, pl.group, pl.tile_tokens))
+      return DYNRAD_ERR_CUDA;
+    if (cache->format == DYNRAD_CACHE_BF16 &&
+        (!encode_pages(&mk, cache->k, cache) || !encode_pages(&mv, cache->v, cache)))
+      return DYNRAD_ERR_CUDA;
 #define DYNRAD_CACHE_F(D_, F_)                                                     \
   rc = pl.tiles == 1 ? launch_cache_attn<D_, F_, 1>(mq, mk, mv, p, ctas, st)       \
                      : launch_cache_attn<D_, F_, 2>(mq, mk, mv, p, ctas, st)
-  DYNRAD_CACHE_DISPATCH(cache->dim, cache->format, DYNRAD_CACHE_F);
+    DYNRAD_CACHE_DISPATCH(cache->dim, cache->format, DYNRAD_CACHE_F);
 #undef DYNRAD_CACHE_F
+  }
   if (rc != DYNRAD_OK || !pl.split) return rc;
   return cache->dim == 128 ? launch_cache_join<128>(p, pl, ctas, st) : launch_cache_join<64>(p, pl, ctas, st);
 }
