@@ -70,6 +70,168 @@ __device__ __forceinline__ uint32_t unpack_pair(uint32_t a, uint32_t b) {
   return sub_bf16x2((w & 0x007f007fu) | 0x43004300u, (w & 0x00800080u) | 0x43004300u);
 }
 
+// What a thread carries through its warp's blocks of a segment.
+template <int D>
+struct TokenState {
+  uint32_t q[2][D / 8];       // Q of rows g and g + 8: of each step its two operand registers
+  float o[D / 8][4];          // O: rows g, g + 8, two columns of each channel tile
+  float m[2], l[2];           // max (log2 units) and this thread's part of the sum
+  int32_t rlo[2], rhi[2];     // what the two rows see
+  int k_off, v_off0, v_off1;  // where it reads (see the kernel)
+};
+
+// Scales whose factor (scale_factors) is the byte shifted; the others (NaN, the
+// least, over 2^7 for e4m3) are rare and send a block the general way.
+template <int FMT>
+__device__ __forceinline__ bool odd_scale(uint32_t byte) {
+  constexpr uint32_t kLeast = FMT == kCacheE4m3 ? 0u : 1u, kMost = FMT == kCacheE4m3 ? 134u : 254u;
+  return byte - kLeast > kMost - kLeast;
+}
+
+template <int FMT, bool ODD>
+__device__ __forceinline__ void block_factors(uint32_t byte, uint32_t& f1, uint32_t& f2) {
+  constexpr uint32_t kBias = FMT == kCacheE4m3 ? 120u : 0u;
+  if (ODD)
+    scale_factors<FMT>(byte, f1, f2);
+  else
+    f1 = byte * 0x00800080u + kBias * 0x00800080u;
+}
+
+// One block of 16 keys from key0 on, its bytes at st.  partial: some row of the item,
+// which sees [lo, hi), does not see all of it.
+template <int D, int FMT, bool ODD>
+__device__ __forceinline__ void token_block(TokenState<D>& me, const uint8_t* st, int key0, bool partial, int32_t lo,
+                                            int32_t hi, float scale_log2, const uint32_t (&kbyte)[2][D / 64],
+                                            uint32_t (&vbyte)[4], volatile int* poison) {
+  constexpr int KW = D / 64, NJ = D / 8, VB = D / 8;
+  using C = CacheTokenCfg<D>;
+  const int t = threadIdx.x & 3;
+  // S = Q K^T: two tiles of eight keys
+  float s[2][4];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) s[n][u] = 0.f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const uint4 x = *reinterpret_cast<const uint4*>(st + n * 8 * D + (w == 0 ? me.k_off : me.k_off ^ 64));
+      uint32_t f1, f2 = kBf16One, a[4], c[4];
+      block_factors<FMT, ODD>(kbyte[n][w], f1, f2);
+      unpack4<FMT>(x.x, a[0], c[0]);
+      unpack4<FMT>(x.y, a[1], c[1]);
+      unpack4<FMT>(x.z, a[2], c[2]);
+      unpack4<FMT>(x.w, a[3], c[3]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        a[u] = mul_bf16x2(a[u], f1);
+        c[u] = mul_bf16x2(c[u], f1);
+        if (ODD) {
+          a[u] = mul_bf16x2(a[u], f2);
+          c[u] = mul_bf16x2(c[u], f2);
+        }
+        mma_16816(s[n], me.q[0][w * 8 + 2 * u], me.q[1][w * 8 + 2 * u], me.q[0][w * 8 + 2 * u + 1], me.q[1][w * 8 + 2 * u + 1],
+                  a[u], c[u]);
+      }
+    }
+  }
+  if (partial) {     // s[n][2 i + e]: row g + 8 i, key 8 n + 4 e + t
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int key = key0 + 8 * n + 4 * (u & 1) + t;
+        if (key < me.rlo[u >> 1] || key >= me.rhi[u >> 1]) s[n][u] = -INFINITY;
+      }
+  }
+  float mx[2], m_new[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) mx[i] = fmaxf(fmax3(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]), s[1][2 * i + 1]);
+#pragma unroll
+  for (int x = 1; x < 4; x <<= 1)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], x));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) m_new[i] = fmaxf(me.m[i], mx[i] * scale_log2);
+  // rescale when a max grew by more than 2^8, the first seen key's block included (m = -inf)
+  if (__any_sync(0xffffffffu, m_new[0] > me.m[0] + 8.0f || m_new[1] > me.m[1] + 8.0f)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool need = m_new[i] > me.m[i] + 8.0f;
+      const float alpha = need ? ex2_approx(me.m[i] - m_new[i]) : 1.0f;
+      if (need) me.m[i] = m_new[i];
+      me.l[i] *= alpha;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        me.o[j][2 * i] *= alpha;
+        me.o[j][2 * i + 1] *= alpha;
+      }
+    }
+  }
+  uint32_t pf[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float ref = me.m[i] == -INFINITY ? 0.f : me.m[i];
+    float e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) e[u] = ex2_approx(fmaf(s[u >> 1][2 * i + (u & 1)], scale_log2, -ref));
+    me.l[i] += (e[0] + e[1]) + (e[2] + e[3]);
+    pf[i] = pack_bf16x2(e[0], e[1]);
+    pf[2 + i] = pack_bf16x2(e[2], e[3]);
+  }
+  // O += P V: V rows t, 4 + t (first operand register), 8 + t, 12 + t (second)
+  uint32_t x[4][VB / 4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint8_t* src = st + ((i & 1) ? me.v_off1 : me.v_off0) + (i >> 1) * 8 * D;
+    if constexpr (D == 128) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src);
+      x[i][0] = v.x;
+      x[i][1] = v.y;
+      x[i][2] = v.z;
+      x[i][3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(src);
+      x[i][0] = v.x;
+      x[i][1] = v.y;
+    }
+  }
+  if (partial) {     // what no row sees, and NaN, stay out of the product (cacheattn.cuh)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = key0 + t + 4 * i;
+      const bool seen = key >= lo && key < hi;
+      if (!seen || vbyte[i] == kCacheNanScale) {
+        if (seen) *poison = 1;
+        vbyte[i] = 127;
+#pragma unroll
+        for (int w = 0; w < VB / 4; ++w) x[i][w] = 0u;
+      }
+    }
+  }
+  uint32_t f1[4], f2[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) block_factors<FMT, ODD>(vbyte[i], f1[i], f2[i]);
+  const uint32_t fa = prmt(f1[0], f1[1], 0x5410u), fb = prmt(f1[2], f1[3], 0x5410u);
+  [[maybe_unused]] const uint32_t ga = ODD ? prmt(f2[0], f2[1], 0x5410u) : 0u, gb = ODD ? prmt(f2[2], f2[3], 0x5410u) : 0u;
+#pragma unroll
+  for (int w = 0; w < VB / 4; ++w) {
+    uint32_t a[4] = {unpack_pair<FMT, 0>(x[0][w], x[1][w]), unpack_pair<FMT, 1>(x[0][w], x[1][w]),
+                     unpack_pair<FMT, 2>(x[0][w], x[1][w]), unpack_pair<FMT, 3>(x[0][w], x[1][w])};
+    uint32_t c[4] = {unpack_pair<FMT, 0>(x[2][w], x[3][w]), unpack_pair<FMT, 1>(x[2][w], x[3][w]),
+                     unpack_pair<FMT, 2>(x[2][w], x[3][w]), unpack_pair<FMT, 3>(x[2][w], x[3][w])};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      a[u] = mul_bf16x2(a[u], fa);
+      c[u] = mul_bf16x2(c[u], fb);
+      if (ODD) {
+        a[u] = mul_bf16x2(a[u], ga);
+        c[u] = mul_bf16x2(c[u], gb);
+      }
+      mma_16816(me.o[4 * w + u], pf[0], pf[1], pf[2], pf[3], a[u], c[u]);
+    }
+  }
+}
+
 template <int D, int FMT>
 __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_kernel(const CacheAttnParams p) {
   using C = CacheTokenCfg<D>;
@@ -104,16 +266,27 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
 
   uint8_t* ring = token_smem + warp * C::kRingBytes;
   const uint32_t ring_u = smem_u32(ring);
-  // where this thread reads: chunk t of its key of the first key tile; its part of V row t
+  // where this thread reads: chunk t of its key of the first key tile; its part of
+  // V rows t and t + 4 (rows t + 8 and t + 12 lie eight rows further on)
   const int krow = (g & 1) * 4 + (g >> 1);
   const int k_off = D == 128 ? krow * 128 + ((t ^ krow) << 4) : g * 64 + (t << 4);
   const int vc = D == 128 ? krow : (g & 1) | ((g & 2) << 1) | ((g & 4) >> 1);   // c(g)
-  // of V row r = t + 4 i (r & 7 = t + 4 (i & 1))
-  auto v_off = [&](int i) -> int {
-    const int r = t + 4 * i;
-    return D == 128 ? r * 128 + ((vc ^ (r & 7)) << 4) : r * 64 + (((vc >> 1) ^ ((r >> 1) & 3)) << 4) + (vc & 1) * 8;
+  auto v_place = [&](int r) -> int {
+    return C::kCodes + (D == 128 ? r * 128 + ((vc ^ r) << 4) : r * 64 + (((vc >> 1) ^ (r >> 1)) << 4) + (vc & 1) * 8);
   };
-  const int v_group = vc * VB / kCacheGroup;
+  const int v_off0 = v_place(t), v_off1 = v_place(t + 4);
+  // scale bytes: of this thread's key and chunk, and of V row t and its channels
+  const int ks_off = 2 * C::kCodes + krow * (D / kCacheGroup) + (t >> 1);
+  const int vs_off = 2 * C::kCodes + C::kScales + t * (D / kCacheGroup) + vc * VB / kCacheGroup;
+  // where this lane's 16-byte chunks of a block go: chunk u = lane + 32 i is row
+  // u / (D / 16); i = 2, 3 (D = 128) lie eight rows further on
+  int k_dst[2], v_dst[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int u = lane + 32 * i, r = u / (D / 16), c = u % (D / 16);
+    k_dst[i] = D == 128 ? r * 128 + ((c ^ r) << 4) : ((r & 8) + (r & 3) * 2 + ((r >> 2) & 1)) * 64 + (c << 4);
+    v_dst[i] = C::kCodes + (D == 128 ? r * 128 + ((c ^ r) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  }
 
   while (left > 0) {
     // the next segment, found by one warp
@@ -167,17 +340,21 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
 
     const int rows = it.ntok * p.group;
     // this thread's rows g and g + 8: what they see, and Q's operands
-    int32_t rlo[2], rhi[2];
-    uint32_t q[2][KW * 8];
+    TokenState<D> me;
+    me.k_off = k_off;
+    me.v_off0 = v_off0;
+    me.v_off1 = v_off1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = g + 8 * i, tok = r / p.group;
-      rlo[i] = 0;
-      rhi[i] = INT32_MAX;     // rows that are not there count as seeing all
+      me.rlo[i] = 0;
+      me.rhi[i] = INT32_MAX;     // rows that are not there count as seeing all
+      me.m[i] = -INFINITY;
+      me.l[i] = 0.f;
 #pragma unroll
-      for (int w = 0; w < KW * 8; ++w) q[i][w] = 0u;
+      for (int w = 0; w < KW * 8; ++w) me.q[i][w] = 0u;
       if (r < rows) {
-        seen_range(p.frame, p.window, it.pos0 + tok, it.len, rlo[i], rhi[i]);
+        seen_range(p.frame, p.window, it.pos0 + tok, it.len, me.rlo[i], me.rhi[i]);
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (it.tok0 + tok) * p.q_token +
                                                           (kvh * p.group + r - tok * p.group) * p.q_head);
 #pragma unroll
@@ -185,19 +362,17 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const uint4 x = src[(t + 4 * w) * 2 + u];
-            q[i][w * 8 + u * 4] = x.x;
-            q[i][w * 8 + u * 4 + 1] = x.y;
-            q[i][w * 8 + u * 4 + 2] = x.z;
-            q[i][w * 8 + u * 4 + 3] = x.w;
+            me.q[i][w * 8 + u * 4] = x.x;
+            me.q[i][w * 8 + u * 4 + 1] = x.y;
+            me.q[i][w * 8 + u * 4 + 2] = x.z;
+            me.q[i][w * 8 + u * 4 + 3] = x.w;
           }
       }
     }
-    float o[NJ][4];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) o[j][u] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int u = 0; u < 4; ++u) me.o[j][u] = 0.f;
 
     // 16-key blocks [b0, b1) of the segment; this warp has b0 + warp, + 6, ..
     const int64_t ka = max(static_cast<int64_t>(it.lo), static_cast<int64_t>(it.step0 + sa) << 7);
@@ -211,16 +386,13 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
         if (!good && lane == 0) record_error(DYNRAD_ERR_DEVICE);
         // a page outside the pool is filled with zeros
         const int64_t row = good ? (((static_cast<int64_t>(pg) * p.c.heads + kvh) << ps) + ((b << 4) & ((1 << ps) - 1))) : 0;
-        const uint8_t* kc = p.c.k + row * D;
-        const uint8_t* vcodes = p.c.v + row * D;
+        const uint8_t* kc = p.c.k + row * D + lane * 16;
+        const uint8_t* vcodes = p.c.v + row * D + lane * 16;
         const uint32_t dst = ring_u + stage * C::kStageBytes;
 #pragma unroll
         for (int i = 0; i < C::kCodes / 512; ++i) {
-          const int u = lane + 32 * i, r = u / (D / 16), c = u % (D / 16);
-          const int kr = D == 128 ? r : (r & 8) + (r & 3) * 2 + ((r >> 2) & 1);
-          const int kcx = D == 128 ? c ^ (r & 7) : c, vcx = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-          cp_async16(dst + kr * D + kcx * 16, kc + u * 16, good);
-          cp_async16(dst + C::kCodes + r * D + vcx * 16, vcodes + u * 16, good);
+          cp_async16(dst + k_dst[i & 1] + (i >> 1) * 1024, kc + i * 512, good);
+          cp_async16(dst + v_dst[i & 1] + (i >> 1) * 1024, vcodes + i * 512, good);
         }
         constexpr int W = C::kScales / 4;     // 16 or 8 words each
         if (lane < 2 * W) {
@@ -245,133 +417,26 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
       __syncwarp();
       const uint8_t* st = ring + stage * C::kStageBytes;
-      const uint8_t* ksc = st + 2 * C::kCodes;
-      const uint8_t* vsc = ksc + C::kScales;
       const int key0 = b << 4;
       const bool partial = key0 < it.lo_max || key0 > it.hi_min - 16;
-      // S = Q K^T: two tiles of eight keys
-      float s[2][4];
+      uint32_t kbyte[2][KW], vbyte[4];
+      bool odd = false;     // a scale whose factor is not its byte shifted (scale_factors)
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) s[n][u] = 0.f;
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const uint4 x = *reinterpret_cast<const uint4*>(st + n * 8 * D + (w == 0 ? k_off : k_off ^ 64));
-          const uint32_t byte = ksc[(n * 8 + krow) * (D / kCacheGroup) + w * 2 + (t >> 1)];
-          uint32_t f1, f2, a[4], c[4];
-          scale_factors<FMT>(byte, f1, f2);
-          unpack4<FMT>(x.x, a[0], c[0]);
-          unpack4<FMT>(x.y, a[1], c[1]);
-          unpack4<FMT>(x.z, a[2], c[2]);
-          unpack4<FMT>(x.w, a[3], c[3]);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            a[u] = mul_bf16x2(a[u], f1);
-            c[u] = mul_bf16x2(c[u], f1);
-          }
-          if (FMT == kCacheE4m3 && __any_sync(0xffffffffu, f2 != kBf16One)) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              a[u] = mul_bf16x2(a[u], f2);
-              c[u] = mul_bf16x2(c[u], f2);
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            mma_16816(s[n], q[0][w * 8 + 2 * u], q[1][w * 8 + 2 * u], q[0][w * 8 + 2 * u + 1], q[1][w * 8 + 2 * u + 1],
-                      a[u], c[u]);
+          kbyte[n][w] = st[ks_off + n * 8 * (D / kCacheGroup) + w * 2];
+          odd = odd || odd_scale<FMT>(kbyte[n][w]);
         }
-      }
-      if (partial) {     // s[n][2 i + e]: row g + 8 i, key 8 n + 4 e + t
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int key = key0 + 8 * n + 4 * (u & 1) + t;
-            if (key < rlo[u >> 1] || key >= rhi[u >> 1]) s[n][u] = -INFINITY;
-          }
-      }
-      uint32_t pf[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx = fmaxf(fmax3(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]), s[1][2 * i + 1]);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float m_new = fmaxf(m[i], mx * p.scale_log2);
-        const bool need = m_new > m[i] + 8.0f;     // the first seen key's block too: m = -inf
-        if (__any_sync(0xffffffffu, need)) {
-          const float alpha = need ? ex2_approx(m[i] - m_new) : 1.0f;
-          if (need) m[i] = m_new;
-          l[i] *= alpha;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            o[j][2 * i] *= alpha;
-            o[j][2 * i + 1] *= alpha;
-          }
-        }
-        const float ref = m[i] == -INFINITY ? 0.f : m[i];
-        float e[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) e[u] = ex2_approx(fmaf(s[u >> 1][2 * i + (u & 1)], p.scale_log2, -ref));
-        l[i] += (e[0] + e[1]) + (e[2] + e[3]);
-        pf[i] = pack_bf16x2(e[0], e[1]);
-        pf[2 + i] = pack_bf16x2(e[2], e[3]);
-      }
-      // O += P V: V rows t, 4 + t (first operand register), 8 + t, 12 + t (second)
-      uint32_t x[4][VB / 4], byte[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint8_t* src = st + C::kCodes + v_off(i);
-        if (D == 128) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src);
-          x[i][0] = v.x;
-          x[i][1] = v.y;
-          x[i][VB / 4 - 2] = v.z;
-          x[i][VB / 4 - 1] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(src);
-          x[i][0] = v.x;
-          x[i][1] = v.y;
-        }
-        byte[i] = vsc[(t + 4 * i) * (D / kCacheGroup) + v_group];
+        vbyte[i] = st[vs_off + i * 4 * (D / kCacheGroup)];
+        odd = odd || odd_scale<FMT>(vbyte[i]);
       }
-      if (partial) {     // what no row sees, and NaN, stay out of the product (cacheattn.cuh)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = key0 + t + 4 * i;
-          const bool seen = key >= it.lo && key < it.hi;
-          if (!seen || byte[i] == kCacheNanScale) {
-            if (seen) *poison = 1;
-            byte[i] = 127;
-#pragma unroll
-            for (int w = 0; w < VB / 4; ++w) x[i][w] = 0u;
-          }
-        }
-      }
-      uint32_t f1[4], f2[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) scale_factors<FMT>(byte[i], f1[i], f2[i]);
-      const uint32_t fa = prmt(f1[0], f1[1], 0x5410u), fb = prmt(f1[2], f1[3], 0x5410u);
-      const bool big = FMT == kCacheE4m3 &&
-          __any_sync(0xffffffffu, f2[0] != kBf16One || f2[1] != kBf16One || f2[2] != kBf16One || f2[3] != kBf16One);
-      const uint32_t ga = prmt(f2[0], f2[1], 0x5410u), gb = prmt(f2[2], f2[3], 0x5410u);
-      auto tile = [&](int j, uint32_t a, uint32_t c) {
-        a = mul_bf16x2(a, fa);
-        c = mul_bf16x2(c, fb);
-        if (big) {
-          a = mul_bf16x2(a, ga);
-          c = mul_bf16x2(c, gb);
-        }
-        mma_16816(o[j], pf[0], pf[1], pf[2], pf[3], a, c);
-      };
-#pragma unroll
-      for (int w = 0; w < VB / 4; ++w) {
-        tile(4 * w, unpack_pair<FMT, 0>(x[0][w], x[1][w]), unpack_pair<FMT, 0>(x[2][w], x[3][w]));
-        tile(4 * w + 1, unpack_pair<FMT, 1>(x[0][w], x[1][w]), unpack_pair<FMT, 1>(x[2][w], x[3][w]));
-        tile(4 * w + 2, unpack_pair<FMT, 2>(x[0][w], x[1][w]), unpack_pair<FMT, 2>(x[2][w], x[3][w]));
-        tile(4 * w + 3, unpack_pair<FMT, 3>(x[0][w], x[1][w]), unpack_pair<FMT, 3>(x[2][w], x[3][w]));
-      }
+      if (__any_sync(0xffffffffu, odd))
+        token_block<D, FMT, true>(me, st, key0, partial, it.lo, it.hi, p.scale_log2, kbyte, vbyte, poison);
+      else
+        token_block<D, FMT, false>(me, st, key0, partial, it.lo, it.hi, p.scale_log2, kbyte, vbyte, poison);
       __syncwarp();      // every lane has read the stage
       load(b + C::kStages * kTokenWarps, next_page, stage);
       next_page = page_of(b + (C::kStages + 1) * kTokenWarps);
@@ -383,10 +448,10 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
     // join the warps: O over their rings
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      me.l[i] += __shfl_xor_sync(0xffffffffu, me.l[i], 1);
+      me.l[i] += __shfl_xor_sync(0xffffffffu, me.l[i], 2);
       const int r = g + 8 * i;
-      if (t == 0) ml[warp * kTokenRows + r] = make_float2(m[i], l[i]);
+      if (t == 0) ml[warp * kTokenRows + r] = make_float2(me.m[i], me.l[i]);
       // columns 2 t and 2 t + 1 of tile j: channels base + j of two runs
       float* dst = reinterpret_cast<float*>(ring) + r * D;
       const int c0 = D == 128 ? 16 * t : 8 * ((((2 * t) & 2) << 1) | (((2 * t) & 4) >> 1));
@@ -394,9 +459,9 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
 #pragma unroll
       for (int j = 0; j < NJ; j += 4) {
         *reinterpret_cast<float4*>(dst + c0 + j) =
-            make_float4(o[j][2 * i], o[j + 1][2 * i], o[j + 2][2 * i], o[j + 3][2 * i]);
+            make_float4(me.o[j][2 * i], me.o[j + 1][2 * i], me.o[j + 2][2 * i], me.o[j + 3][2 * i]);
         *reinterpret_cast<float4*>(dst + c1 + j) =
-            make_float4(o[j][2 * i + 1], o[j + 1][2 * i + 1], o[j + 2][2 * i + 1], o[j + 3][2 * i + 1]);
+            make_float4(me.o[j][2 * i + 1], me.o[j + 1][2 * i + 1], me.o[j + 2][2 * i + 1], me.o[j + 3][2 * i + 1]);
       }
     }
     __syncthreads();
