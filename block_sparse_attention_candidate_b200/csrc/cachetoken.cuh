@@ -5,28 +5,33 @@
 // The tensor-core tiles of cacheattn.cuh want bf16 operands in shared memory.  For
 // few rows that detour is the bound: 64 KB written and 96 KB read again by the
 // products for every 33 KB of 128 keys.  Here a warp turns the stored bytes into
-// register fragments of a 16 x 8 x 16 product (warp_mma.cuh) and nothing goes
-// back: shared memory holds the bytes alone, once written and once read.
-// Measured (3 sequences of 131,072 keys, 8 K / V heads, e4m3): see cache_token_kernel.
+// register fragments of 16 x 8 x 16 products (warp_mma.cuh) and nothing goes back:
+// shared memory holds the bytes alone, once written and once read.
 //
-// Fragments without a shuffle.  The product sums over channels (Q K^T) or keys
-// (P V) in any order and its columns may be any keys or channels, so they are named
-// to suit 16-byte reads (thread 4 g + t of the warp):
-//   Q K^T  column g of key tile n is key 8 n + 4 (g & 1) + g / 2; thread t has the
-//          16 channels of chunk t (and t + 4): word kk of it is step kk's operand;
-//   P V    the sums over keys run over 16 keys in the order that leaves each
-//          thread's S where P's operand wants it: keys t, 4 + t, 8 + t, 12 + t;
-//          column g of channel tile j is channel 16 c(g) + j (8 c(g) + j at D = 64),
-//          byte j of what the thread read.
+// The keys are the products' 16 rows, since there are more of them than query rows:
+// S^T = K Q^T and O^T = V^T P^T, with 8 query rows a column tile (NT = 1 or 2 of
+// them).  Eight rows then cost half the products and accumulators of the other way
+// round, and the registers so freed hold more warps, which hide the unpacking.
+//
+// Fragments without a shuffle.  The products sum over channels (K Q^T) or keys
+// (V^T P^T) in any order and their rows may be any keys or channels, so they are
+// named to suit 16-byte reads (thread 4 g + t of the warp):
+//   K Q^T    rows g and g + 8 are the keys k = 4 (g & 1) + g / 2 and k + 8; thread t
+//            has the 16 channels of chunk t (and t + 4): word u of it is step u's
+//            operand;
+//   V^T P^T  P^T, transposed by movmatrix, sums over the keys t, 4 + t, 8 + t,
+//            12 + t; rows g and g + 8 of channel tile j are the channels
+//            16 c(g) + 2 j and + 1 (8 c(g) + .. at D = 64), bytes 2 j and 2 j + 1 of
+//            what the thread read.
 // The bytes lie in shared memory so that the threads served together meet
 // different banks: 16-byte chunk c of row r at c ^ (r & 7) (D = 128).  At D = 64, K's
 // row r takes place 2 (r & 3) + r / 4 of its eight and V's chunk c is at
 // c ^ ((r / 2) & 3).
 //
-// A CTA has six warps and an SM two CTAs; a segment's 16-key blocks go to the warps
-// in turn, each warp with a ring of its own, filled by cp.async, and its own max, sum
-// and O.  At the end of a segment the six are joined in shared memory while the
-// SM's other CTA reads on.
+// A CTA has eight warps and an SM three CTAs (NT = 1) or two; a segment's 16-key
+// blocks go to the warps in turn, each warp with a ring of its own, filled by
+// cp.async, and its own max, sum and O.  At the end of a segment the eight are joined
+// in shared memory while the SM's other CTAs read on.
 #pragma once
 
 #include "cacheattn.cuh"
@@ -34,23 +39,24 @@
 
 namespace dynrad {
 
-constexpr int kTokenRows = 16;       // rows of an item
-constexpr int kTokenWarps = 6;
+constexpr int kTokenWarps = 8;
 constexpr int kTokenThreads = kTokenWarps * 32;
-constexpr int kTokenCtasPerSm = 2;
 constexpr int kTokenKeys = 16;       // keys of a block
 
-template <int D>
+template <int D, int NT>
 struct CacheTokenCfg {
+  static constexpr int kRows = 8 * NT;                          // rows of an item
+  static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
   static constexpr int kCodes = kTokenKeys * D;
   static constexpr int kScales = kTokenKeys * (D / kCacheGroup);
   static constexpr int kStageBytes = 2 * (kCodes + kScales);    // K, V, K's scales, V's scales
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStages = (NT == 1 ? 2 : 3) * (128 / D);
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kOut = kTokenRows * D * 4;               // a warp's O, over its ring
-  static constexpr int kSmem = kTokenWarps * kRingBytes + 2048;
-  static_assert(kOut <= kRingBytes, "O over the ring");
-  static_assert(kTokenCtasPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+  static constexpr int kQ = NT * (D / 16) * 256;                // Q's operands, 8 bytes a step and lane
+  static constexpr int kCtrl = 256 + kTokenWarps * kRows * 8;
+  static constexpr int kSmem = kTokenWarps * kRingBytes + kQ + kCtrl;
+  static_assert(kRows * D * 4 <= kRingBytes, "a warp's O over its ring");
+  static_assert(kCtasPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
@@ -60,125 +66,128 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool fi
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(fill ? 4 : 0) : "memory");
 }
 
-// Byte k of a (in the low half) and of b -> a bf16 pair, before their scales
-// (unpack4 with the bytes of two words).
+// 8 x 8 matrix of 16-bit values, a row of pairs in threads 4 r .. 4 r + 3: transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Byte K of a (in the low half) and of b -> a bf16 pair, before their scales: unpack4
+// with the bytes of two words.  flip: 0x00800080, kept in a register.
 template <int FMT, int K>
-__device__ __forceinline__ uint32_t unpack_pair(uint32_t a, uint32_t b) {
-  constexpr uint32_t kSel = ((4u + K) << 12) | ((8u | K) << 8) | (K << 4) | K;
-  if (FMT == kCacheE4m3) return static_cast<uint32_t>(static_cast<int32_t>(prmt(a, b, kSel)) >> 4) & 0x87f087f0u;
-  const uint32_t w = prmt(a, b, ((4u + K) << 8) | (4u + K) << 12 | (K << 4) | K);
-  return sub_bf16x2((w & 0x007f007fu) | 0x43004300u, (w & 0x00800080u) | 0x43004300u);
+__device__ __forceinline__ uint32_t unpack_pair(uint32_t a, uint32_t b, uint32_t flip) {
+  if (FMT == kCacheE4m3) {
+    constexpr uint32_t kSel = ((4u + K) << 12) | ((8u | K) << 8) | (K << 4) | K;
+    return static_cast<uint32_t>(static_cast<int32_t>(prmt(a, b, kSel)) >> 4) & 0x87f087f0u;
+  }
+  constexpr uint32_t kSel = ((4u + K) << 12) | ((4u + K) << 8) | (K << 4) | K;
+  return bytes_to_bf16x2((prmt(a, b, kSel) & 0x00ff00ffu) ^ flip);
 }
 
 // What a thread carries through its warp's blocks of a segment.
-template <int D>
+template <int D, int NT>
 struct TokenState {
-  uint32_t q[2][D / 8];       // Q of rows g and g + 8: of each step its two operand registers
-  float o[D / 8][4];          // O: rows g, g + 8, two columns of each channel tile
-  float m[2], l[2];           // max (log2 units) and this thread's part of the sum
-  int32_t rlo[2], rhi[2];     // what the two rows see
-  int k_off, v_off0, v_off1;  // where it reads (see the kernel)
+  float o[NT][D / 16][4];     // O^T: of channel tile j rows g, g + 8; query rows 2 t, 2 t + 1
+  float m[NT][2], l[NT][2];   // of query rows 2 t, 2 t + 1: max (log2 units), this thread's part of the sum
+  int32_t rlo[NT][2], rhi[NT][2];   // what those rows see
+  int k_off, v_off0, v_off1;  // where the thread reads (see the kernel)
+  uint32_t flip;              // unpack_pair's constant
 };
 
-// Scales whose factor (scale_factors) is the byte shifted; the others (NaN, the
-// least, over 2^7 for e4m3) are rare and send a block the general way.
-template <int FMT>
-__device__ __forceinline__ bool odd_scale(uint32_t byte) {
-  constexpr uint32_t kLeast = FMT == kCacheE4m3 ? 0u : 1u, kMost = FMT == kCacheE4m3 ? 134u : 254u;
-  return byte - kLeast > kMost - kLeast;
-}
-
-template <int FMT, bool ODD>
-__device__ __forceinline__ void block_factors(uint32_t byte, uint32_t& f1, uint32_t& f2) {
-  constexpr uint32_t kBias = FMT == kCacheE4m3 ? 120u : 0u;
-  if (ODD)
-    scale_factors<FMT>(byte, f1, f2);
-  else
-    f1 = byte * 0x00800080u + kBias * 0x00800080u;
-}
-
 // One block of 16 keys from key0 on, its bytes at st.  partial: some row of the item,
-// which sees [lo, hi), does not see all of it.
-template <int D, int FMT, bool ODD>
-__device__ __forceinline__ void token_block(TokenState<D>& me, const uint8_t* st, int key0, bool partial, int32_t lo,
-                                            int32_t hi, float scale_log2, const uint32_t (&kbyte)[2][D / 64],
-                                            uint32_t (&vbyte)[4], volatile int* poison) {
-  constexpr int KW = D / 64, NJ = D / 8, VB = D / 8;
-  using C = CacheTokenCfg<D>;
-  const int t = threadIdx.x & 3;
-  // S = Q K^T: two tiles of eight keys
-  float s[2][4];
+// which sees [lo, hi), does not see all of it.  odd: some scale's factor takes more
+// than a shift of its byte (odd_scale); such blocks are rare.
+template <int D, int FMT, int NT>
+__device__ __forceinline__ void token_block(TokenState<D, NT>& me, const uint8_t* st, int key0, bool partial, bool odd,
+                                            int32_t lo, int32_t hi, float scale_log2, const uint32_t (&kbyte)[2][D / 64],
+                                            uint32_t (&vbyte)[4], const uint2* qs, volatile int* poison) {
+  constexpr int KW = D / 64, VB = D / 8, NJ = D / 16;
+  using C = CacheTokenCfg<D, NT>;
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  // S^T = K Q^T
+  float s[NT][4] = {};
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
+  for (int w = 0; w < KW; ++w) {
+    uint32_t kf[2][2][4];     // [key row][operand register][step]
 #pragma unroll
-    for (int u = 0; u < 4; ++u) s[n][u] = 0.f;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) {
+    for (int n = 0; n < 2; ++n) {
       const uint4 x = *reinterpret_cast<const uint4*>(st + n * 8 * D + (w == 0 ? me.k_off : me.k_off ^ 64));
-      uint32_t f1, f2 = kBf16One, a[4], c[4];
-      block_factors<FMT, ODD>(kbyte[n][w], f1, f2);
-      unpack4<FMT>(x.x, a[0], c[0]);
-      unpack4<FMT>(x.y, a[1], c[1]);
-      unpack4<FMT>(x.z, a[2], c[2]);
-      unpack4<FMT>(x.w, a[3], c[3]);
+      const uint32_t f = odd ? kBf16One : kbyte[n][w] * 0x00800080u + kUnpackBias<FMT> * 0x00800080u;
+      unpack4<FMT>(x.x, kf[n][0][0], kf[n][1][0]);
+      unpack4<FMT>(x.y, kf[n][0][1], kf[n][1][1]);
+      unpack4<FMT>(x.z, kf[n][0][2], kf[n][1][2]);
+      unpack4<FMT>(x.w, kf[n][0][3], kf[n][1][3]);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        a[u] = mul_bf16x2(a[u], f1);
-        c[u] = mul_bf16x2(c[u], f1);
-        if (ODD) {
-          a[u] = mul_bf16x2(a[u], f2);
-          c[u] = mul_bf16x2(c[u], f2);
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) kf[n][e][u] = mul_bf16x2(kf[n][e][u], f);
+    }
+    if (odd) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        uint32_t f1, f2;
+        scale_factors<FMT>(kbyte[n][w], f1, f2);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) kf[n][e][u] = mul_bf16x2(mul_bf16x2(kf[n][e][u], f1), f2);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint2 q = qs[(n * NJ + w * 4 + u) * 32];
+        mma_16816(s[n], kf[0][0][u], kf[1][0][u], kf[0][1][u], kf[1][1][u], q.x, q.y);
+      }
+  }
+  // s[n][2 i + e]: key 8 i + 4 (g & 1) + g / 2, query row 8 n + 2 t + e
+  if (partial) {
+    const int key = key0 + 4 * (g & 1) + (g >> 1);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (key + 8 * (u >> 1) < me.rlo[n][u & 1] || key + 8 * (u >> 1) >= me.rhi[n][u & 1]) s[n][u] = -INFINITY;
+  }
+  uint32_t pf[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float mx[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])}, m_new[2];
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], x));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) m_new[e] = fmaxf(me.m[n][e], mx[e] * scale_log2);
+    // rescale when a max grew by more than 2^8, the first seen key's block included (m = -inf)
+    if (__any_sync(0xffffffffu, m_new[0] > me.m[n][0] + 8.0f || m_new[1] > me.m[n][1] + 8.0f)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool need = m_new[e] > me.m[n][e] + 8.0f;
+        const float alpha = need ? ex2_approx(me.m[n][e] - m_new[e]) : 1.0f;
+        if (need) me.m[n][e] = m_new[e];
+        me.l[n][e] *= alpha;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          me.o[n][j][e] *= alpha;
+          me.o[n][j][2 + e] *= alpha;
         }
-        mma_16816(s[n], me.q[0][w * 8 + 2 * u], me.q[1][w * 8 + 2 * u], me.q[0][w * 8 + 2 * u + 1], me.q[1][w * 8 + 2 * u + 1],
-                  a[u], c[u]);
       }
     }
-  }
-  if (partial) {     // s[n][2 i + e]: row g + 8 i, key 8 n + 4 e + t
+    float p[4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int e = 0; e < 2; ++e) {
+      const float ref = me.m[n][e] == -INFINITY ? 0.f : me.m[n][e];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int key = key0 + 8 * n + 4 * (u & 1) + t;
-        if (key < me.rlo[u >> 1] || key >= me.rhi[u >> 1]) s[n][u] = -INFINITY;
-      }
-  }
-  float mx[2], m_new[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) mx[i] = fmaxf(fmax3(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]), s[1][2 * i + 1]);
-#pragma unroll
-  for (int x = 1; x < 4; x <<= 1)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], x));
-#pragma unroll
-  for (int i = 0; i < 2; ++i) m_new[i] = fmaxf(me.m[i], mx[i] * scale_log2);
-  // rescale when a max grew by more than 2^8, the first seen key's block included (m = -inf)
-  if (__any_sync(0xffffffffu, m_new[0] > me.m[0] + 8.0f || m_new[1] > me.m[1] + 8.0f)) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool need = m_new[i] > me.m[i] + 8.0f;
-      const float alpha = need ? ex2_approx(me.m[i] - m_new[i]) : 1.0f;
-      if (need) me.m[i] = m_new[i];
-      me.l[i] *= alpha;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        me.o[j][2 * i] *= alpha;
-        me.o[j][2 * i + 1] *= alpha;
-      }
+      for (int i = 0; i < 2; ++i) p[2 * i + e] = ex2_approx(fmaf(s[n][2 * i + e], scale_log2, -ref));
+      me.l[n][e] += p[e] + p[2 + e];
     }
+    pf[n][0] = transpose8x8(pack_bf16x2(p[0], p[1]));
+    pf[n][1] = transpose8x8(pack_bf16x2(p[2], p[3]));
   }
-  uint32_t pf[4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float ref = me.m[i] == -INFINITY ? 0.f : me.m[i];
-    float e[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) e[u] = ex2_approx(fmaf(s[u >> 1][2 * i + (u & 1)], scale_log2, -ref));
-    me.l[i] += (e[0] + e[1]) + (e[2] + e[3]);
-    pf[i] = pack_bf16x2(e[0], e[1]);
-    pf[2 + i] = pack_bf16x2(e[2], e[3]);
-  }
-  // O += P V: V rows t, 4 + t (first operand register), 8 + t, 12 + t (second)
+  // O^T += V^T P^T: V rows t, 4 + t (first keys of the sum), 8 + t, 12 + t
   uint32_t x[4][VB / 4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -208,43 +217,56 @@ __device__ __forceinline__ void token_block(TokenState<D>& me, const uint8_t* st
       }
     }
   }
-  uint32_t f1[4], f2[4];
+  uint32_t f1[4], f2[4] = {kBf16One, kBf16One, kBf16One, kBf16One};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) block_factors<FMT, ODD>(vbyte[i], f1[i], f2[i]);
+  for (int i = 0; i < 4; ++i) f1[i] = vbyte[i] * 0x00800080u + kUnpackBias<FMT> * 0x00800080u;
+  if (odd) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) scale_factors<FMT>(vbyte[i], f1[i], f2[i]);
+  }
   const uint32_t fa = prmt(f1[0], f1[1], 0x5410u), fb = prmt(f1[2], f1[3], 0x5410u);
-  [[maybe_unused]] const uint32_t ga = ODD ? prmt(f2[0], f2[1], 0x5410u) : 0u, gb = ODD ? prmt(f2[2], f2[3], 0x5410u) : 0u;
+  const uint32_t ga = prmt(f2[0], f2[1], 0x5410u), gb = prmt(f2[2], f2[3], 0x5410u);
 #pragma unroll
   for (int w = 0; w < VB / 4; ++w) {
-    uint32_t a[4] = {unpack_pair<FMT, 0>(x[0][w], x[1][w]), unpack_pair<FMT, 1>(x[0][w], x[1][w]),
-                     unpack_pair<FMT, 2>(x[0][w], x[1][w]), unpack_pair<FMT, 3>(x[0][w], x[1][w])};
-    uint32_t c[4] = {unpack_pair<FMT, 0>(x[2][w], x[3][w]), unpack_pair<FMT, 1>(x[2][w], x[3][w]),
-                     unpack_pair<FMT, 2>(x[2][w], x[3][w]), unpack_pair<FMT, 3>(x[2][w], x[3][w])};
+    uint32_t a[4] = {unpack_pair<FMT, 0>(x[0][w], x[1][w], me.flip), unpack_pair<FMT, 1>(x[0][w], x[1][w], me.flip),
+                     unpack_pair<FMT, 2>(x[0][w], x[1][w], me.flip), unpack_pair<FMT, 3>(x[0][w], x[1][w], me.flip)};
+    uint32_t c[4] = {unpack_pair<FMT, 0>(x[2][w], x[3][w], me.flip), unpack_pair<FMT, 1>(x[2][w], x[3][w], me.flip),
+                     unpack_pair<FMT, 2>(x[2][w], x[3][w], me.flip), unpack_pair<FMT, 3>(x[2][w], x[3][w], me.flip)};
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       a[u] = mul_bf16x2(a[u], fa);
       c[u] = mul_bf16x2(c[u], fb);
-      if (ODD) {
+    }
+    if (odd) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
         a[u] = mul_bf16x2(a[u], ga);
         c[u] = mul_bf16x2(c[u], gb);
       }
-      mma_16816(me.o[4 * w + u], pf[0], pf[1], pf[2], pf[3], a[u], c[u]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      mma_16816(me.o[n][2 * w], a[0], a[1], c[0], c[1], pf[n][0], pf[n][1]);
+      mma_16816(me.o[n][2 * w + 1], a[2], a[3], c[2], c[3], pf[n][0], pf[n][1]);
     }
   }
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_kernel(const CacheAttnParams p) {
-  using C = CacheTokenCfg<D>;
-  constexpr int KW = D == 128 ? 2 : 1;       // 16-byte chunks of a key that a thread reads
-  constexpr int NJ = D / 8;                  // channel tiles
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerSm)
+    cache_token_kernel(const CacheAttnParams p) {
+  using C = CacheTokenCfg<D, NT>;
+  constexpr int KW = D / 64;                 // 16-byte chunks of a key that a thread reads
   constexpr int VB = D / 8;                  // bytes of a V row that a thread reads: 16 or 8
+  constexpr int NJ = D / 16;                 // channel tiles, and steps of K Q^T
   extern __shared__ __align__(128) uint8_t token_smem[];
-  uint8_t* ctrl = token_smem + kTokenWarps * C::kRingBytes;
-  CacheRun* run = reinterpret_cast<CacheRun*>(ctrl);                       // 24 bytes
+  uint2* q_s = reinterpret_cast<uint2*>(token_smem + kTokenWarps * C::kRingBytes);   // [row tile][step][lane]
+  uint8_t* ctrl = token_smem + kTokenWarps * C::kRingBytes + C::kQ;
+  CacheRun* run = reinterpret_cast<CacheRun*>(ctrl);
   volatile int* poison = reinterpret_cast<volatile int*>(ctrl + 32);
   CacheSeg* seg_s = reinterpret_cast<CacheSeg*>(ctrl + 64);
-  float2* ml = reinterpret_cast<float2*>(ctrl + 256);                      // [warp][row]
-  static_assert(64 + sizeof(CacheSeg) <= 256 && 256 + kTokenWarps * kTokenRows * 8 <= 2048, "control block");
+  float2* ml = reinterpret_cast<float2*>(ctrl + 256);                                // [warp][row]
+  static_assert(sizeof(CacheRun) <= 32 && 64 + sizeof(CacheSeg) <= 256, "control block");
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -266,15 +288,18 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
 
   uint8_t* ring = token_smem + warp * C::kRingBytes;
   const uint32_t ring_u = smem_u32(ring);
-  // where this thread reads: chunk t of its key of the first key tile; its part of
-  // V rows t and t + 4 (rows t + 8 and t + 12 lie eight rows further on)
+  TokenState<D, NT> me;
+  // where this thread reads: chunk t of its first key; its part of V rows t and t + 4
+  // (rows t + 8 and t + 12 lie eight rows further on)
   const int krow = (g & 1) * 4 + (g >> 1);
-  const int k_off = D == 128 ? krow * 128 + ((t ^ krow) << 4) : g * 64 + (t << 4);
+  me.k_off = D == 128 ? krow * 128 + ((t ^ krow) << 4) : g * 64 + (t << 4);
   const int vc = D == 128 ? krow : (g & 1) | ((g & 2) << 1) | ((g & 4) >> 1);   // c(g)
   auto v_place = [&](int r) -> int {
     return C::kCodes + (D == 128 ? r * 128 + ((vc ^ r) << 4) : r * 64 + (((vc >> 1) ^ (r >> 1)) << 4) + (vc & 1) * 8);
   };
-  const int v_off0 = v_place(t), v_off1 = v_place(t + 4);
+  me.v_off0 = v_place(t);
+  me.v_off1 = v_place(t + 4);
+  me.flip = 0x00800080u ^ (gridDim.z - 1u);   // gridDim.z is 1: a constant that stays in a register
   // scale bytes: of this thread's key and chunk, and of V row t and its channels
   const int ks_off = 2 * C::kCodes + krow * (D / kCacheGroup) + (t >> 1);
   const int vs_off = 2 * C::kCodes + C::kScales + t * (D / kCacheGroup) + vc * VB / kCacheGroup;
@@ -339,42 +364,7 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
     left = seg_s->narrow ? max(left, static_cast<int64_t>(1)) : 0;   // warp 0 keeps the count
 
     const int rows = it.ntok * p.group;
-    // this thread's rows g and g + 8: what they see, and Q's operands
-    TokenState<D> me;
-    me.k_off = k_off;
-    me.v_off0 = v_off0;
-    me.v_off1 = v_off1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i, tok = r / p.group;
-      me.rlo[i] = 0;
-      me.rhi[i] = INT32_MAX;     // rows that are not there count as seeing all
-      me.m[i] = -INFINITY;
-      me.l[i] = 0.f;
-#pragma unroll
-      for (int w = 0; w < KW * 8; ++w) me.q[i][w] = 0u;
-      if (r < rows) {
-        seen_range(p.frame, p.window, it.pos0 + tok, it.len, me.rlo[i], me.rhi[i]);
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (it.tok0 + tok) * p.q_token +
-                                                          (kvh * p.group + r - tok * p.group) * p.q_head);
-#pragma unroll
-        for (int w = 0; w < KW; ++w)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint4 x = src[(t + 4 * w) * 2 + u];
-            me.q[i][w * 8 + u * 4] = x.x;
-            me.q[i][w * 8 + u * 4 + 1] = x.y;
-            me.q[i][w * 8 + u * 4 + 2] = x.z;
-            me.q[i][w * 8 + u * 4 + 3] = x.w;
-          }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) me.o[j][u] = 0.f;
-
-    // 16-key blocks [b0, b1) of the segment; this warp has b0 + warp, + 6, ..
+    // 16-key blocks [b0, b1) of the segment; this warp has b0 + warp, + 8, ..
     const int64_t ka = max(static_cast<int64_t>(it.lo), static_cast<int64_t>(it.step0 + sa) << 7);
     const int64_t kb = min(static_cast<int64_t>(it.hi), static_cast<int64_t>(it.step0 + sb) << 7);
     const int b0 = static_cast<int>(ka >> 4), b1 = sb > sa ? static_cast<int>((kb + 15) >> 4) : b0;
@@ -411,6 +401,36 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
       for (int s = 0; s < C::kStages; ++s) load(b + s * kTokenWarps, pg[s], s);
     }
     int32_t next_page = page_of(b + C::kStages * kTokenWarps);
+
+    // Q's operands: query row 8 n + g, step u: of chunk t + 4 (u / 4) the channels of
+    // word u % 4; a warp brings a step
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = 8 * n + g, tok = r / p.group;
+      if (warp < NJ) {
+        uint2 q = make_uint2(0u, 0u);
+        if (r < rows)
+          q = *reinterpret_cast<const uint2*>(p.q + (it.tok0 + tok) * p.q_token +
+                                              (kvh * p.group + r - tok * p.group) * p.q_head +
+                                              (t + 4 * (warp >> 2)) * 16 + (warp & 3) * 4);
+        q_s[(n * NJ + warp) * 32 + lane] = q;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
+        me.rlo[n][e] = 0;
+        me.rhi[n][e] = INT32_MAX;     // rows that are not there count as seeing all
+        if (r < rows) seen_range(p.frame, p.window, it.pos0 + r / p.group, it.len, me.rlo[n][e], me.rhi[n][e]);
+        me.m[n][e] = -INFINITY;
+        me.l[n][e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) me.o[n][j][e] = me.o[n][j][2 + e] = 0.f;
+      }
+    __syncthreads();
+
     int stage = 0;
 #pragma unroll 1
     for (; b < b1; b += kTokenWarps) {
@@ -420,7 +440,7 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
       const int key0 = b << 4;
       const bool partial = key0 < it.lo_max || key0 > it.hi_min - 16;
       uint32_t kbyte[2][KW], vbyte[4];
-      bool odd = false;     // a scale whose factor is not its byte shifted (scale_factors)
+      bool odd = false;
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -433,10 +453,8 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
         vbyte[i] = st[vs_off + i * 4 * (D / kCacheGroup)];
         odd = odd || odd_scale<FMT>(vbyte[i]);
       }
-      if (__any_sync(0xffffffffu, odd))
-        token_block<D, FMT, true>(me, st, key0, partial, it.lo, it.hi, p.scale_log2, kbyte, vbyte, poison);
-      else
-        token_block<D, FMT, false>(me, st, key0, partial, it.lo, it.hi, p.scale_log2, kbyte, vbyte, poison);
+      token_block<D, FMT, NT>(me, st, key0, partial, __any_sync(0xffffffffu, odd), it.lo, it.hi, p.scale_log2, kbyte,
+                              vbyte, q_s + lane, poison);
       __syncwarp();      // every lane has read the stage
       load(b + C::kStages * kTokenWarps, next_page, stage);
       next_page = page_of(b + (C::kStages + 1) * kTokenWarps);
@@ -447,34 +465,30 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
 
     // join the warps: O over their rings
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      me.l[i] += __shfl_xor_sync(0xffffffffu, me.l[i], 1);
-      me.l[i] += __shfl_xor_sync(0xffffffffu, me.l[i], 2);
-      const int r = g + 8 * i;
-      if (t == 0) ml[warp * kTokenRows + r] = make_float2(me.m[i], me.l[i]);
-      // columns 2 t and 2 t + 1 of tile j: channels base + j of two runs
-      float* dst = reinterpret_cast<float*>(ring) + r * D;
-      const int c0 = D == 128 ? 16 * t : 8 * ((((2 * t) & 2) << 1) | (((2 * t) & 4) >> 1));
-      const int c1 = D == 128 ? 64 + 16 * t : c0 + 8;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < NJ; j += 4) {
-        *reinterpret_cast<float4*>(dst + c0 + j) =
-            make_float4(me.o[j][2 * i], me.o[j + 1][2 * i], me.o[j + 2][2 * i], me.o[j + 3][2 * i]);
-        *reinterpret_cast<float4*>(dst + c1 + j) =
-            make_float4(me.o[j][2 * i + 1], me.o[j + 1][2 * i + 1], me.o[j + 2][2 * i + 1], me.o[j + 3][2 * i + 1]);
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) me.l[n][e] += __shfl_xor_sync(0xffffffffu, me.l[n][e], x);
+        const int r = 8 * n + 2 * t + e;
+        if (g == 0) ml[warp * C::kRows + r] = make_float2(me.m[n][e], me.l[n][e]);
+        float* dst = reinterpret_cast<float*>(ring) + r * D + vc * VB;   // the thread's run of channels
+#pragma unroll
+        for (int j = 0; j < NJ; j += 2)
+          *reinterpret_cast<float4*>(dst + 2 * j) =
+              make_float4(me.o[n][j][e], me.o[n][j][2 + e], me.o[n][j + 1][e], me.o[n][j + 1][2 + e]);
       }
-    }
     __syncthreads();
     const bool poisoned = *poison != 0;
     for (int u = threadIdx.x; u < rows * (D / 4); u += kTokenThreads) {
       const int r = u / (D / 4), c = u % (D / 4);
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-      for (int w = 0; w < kTokenWarps; ++w) mm = fmaxf(mm, ml[w * kTokenRows + r].x);
+      for (int w = 0; w < kTokenWarps; ++w) mm = fmaxf(mm, ml[w * C::kRows + r].x);
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kTokenWarps; ++w) {
-        const float2 x = ml[w * kTokenRows + r];
+        const float2 x = ml[w * C::kRows + r];
         const float f = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2_approx(x.x - mm);
         if (f == 0.f) continue;
         const float4 v = reinterpret_cast<const float4*>(token_smem + w * C::kRingBytes + r * (D * 4))[c];
@@ -500,7 +514,7 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenCtasPerSm) cache_token_ke
       }
       const int64_t token = it.tok0 + tok;
       if (part >= 0) {
-        const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + part) * kTokenRows + r;
+        const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + part) * C::kRows + r;
         reinterpret_cast<float4*>(p.part_o + prow * D)[c] = a;
         if (c == 0) p.part_ml[prow] = make_float2(mm, ll);
       } else {

@@ -1228,7 +1228,8 @@ namespace {
 struct CachePlan {
   int32_t group, tile_tokens, tiles, item_tokens, slots;
   int32_t part_rows, ctas_per_sm;
-  bool token, split;   // token: cachetoken.cuh's kernel
+  int32_t token_tiles;   // column tiles of cachetoken.cuh's kernel; 0: cacheattn.cuh's
+  bool split;
   size_t part_ml, part_desc, total;
 };
 
@@ -1239,16 +1240,20 @@ int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, i
   pl->group = heads / c->heads;
   if (pl->group > 128) return DYNRAD_ERR_UNSUPPORTED;
   pl->tile_tokens = 128 / pl->group;
-  // 8-bit pages and sequences of 16 rows or fewer on average: the kernel that reads
-  // them once (TOKEN_FIGURES)
-  pl->token = c->format != DYNRAD_CACHE_BF16 && pl->group <= kTokenRows &&
-              static_cast<int64_t>(num_tokens) <= static_cast<int64_t>(num_seqs) * (kTokenRows / pl->group);
-  if (pl->token) pl->tile_tokens = kTokenRows / pl->group;
+  // 8-bit pages and sequences of 8 or 16 rows on average at most: the kernel that
+  // reads them once (TOKEN_FIGURES)
+  pl->token_tiles = 0;
+  for (int nt = 2; nt >= 1; --nt)
+    if (c->format != DYNRAD_CACHE_BF16 && pl->group <= 8 * nt &&
+        static_cast<int64_t>(num_tokens) <= static_cast<int64_t>(num_seqs) * (8 * nt / pl->group))
+      pl->token_tiles = nt;
+  if (pl->token_tiles > 0) pl->tile_tokens = 8 * pl->token_tiles / pl->group;
   // one tile an item where the sequences' tokens fill no more on average
   pl->tiles = static_cast<int64_t>(num_tokens) <= static_cast<int64_t>(num_seqs) * pl->tile_tokens ? 1 : 2;
   pl->item_tokens = pl->tiles * pl->tile_tokens;
-  pl->part_rows = pl->token ? kTokenRows : 128 * pl->tiles;
-  pl->ctas_per_sm = pl->token ? kTokenCtasPerSm : 1;
+  pl->part_rows = pl->token_tiles > 0 ? 8 * pl->token_tiles : 128 * pl->tiles;
+  pl->ctas_per_sm = pl->token_tiles == 0 ? 1 : (pl->token_tiles == 1 ? CacheTokenCfg<128, 1>::kCtasPerSm
+                                                                      : CacheTokenCfg<128, 2>::kCtasPerSm);
   const int64_t slots = static_cast<int64_t>(num_tokens) / pl->item_tokens + num_seqs;
   if (slots > INT32_MAX || c->heads > 65535) return DYNRAD_ERR_UNSUPPORTED;
   pl->slots = static_cast<int32_t>(slots);
@@ -1305,15 +1310,20 @@ int launch_cache_attn(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
   return launch_status();
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int NT>
 int launch_cache_token(const CacheAttnParams& p, int ctas, cudaStream_t st) {
-  using C = CacheTokenCfg<D>;
+  using C = CacheTokenCfg<D, NT>;
   static OptInTable optin;   // per instantiation, per device
-  const int rc = smem_optin(optin, reinterpret_cast<const void*>(cache_token_kernel<D, FMT>), C::kSmem);
+  const int rc = smem_optin(optin, reinterpret_cast<const void*>(cache_token_kernel<D, FMT, NT>), C::kSmem);
   if (rc != DYNRAD_OK) return rc;
   const dim3 grid = p.split ? dim3(ctas) : dim3(p.slots, p.c.heads);
-  cache_token_kernel<D, FMT><<<grid, kTokenThreads, C::kSmem, st>>>(p);
+  cache_token_kernel<D, FMT, NT><<<grid, kTokenThreads, C::kSmem, st>>>(p);
   return launch_status();
+}
+
+template <int D, int FMT>
+int launch_cache_token(const CacheAttnParams& p, int tiles, int ctas, cudaStream_t st) {
+  return tiles == 1 ? launch_cache_token<D, FMT, 1>(p, ctas, st) : launch_cache_token<D, FMT, 2>(p, ctas, st);
 }
 
 template <int D>
@@ -1391,12 +1401,15 @@ extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs
     return DYNRAD_ERR_CUDA;
   const int ctas = std::min(sms, kCacheMaxCtas) * pl.ctas_per_sm;
   cudaStream_t st = as_stream(stream);
-  if (pl.token) {
+  if (pl.token_tiles > 0) {
     const bool e4m3 = cache->format == DYNRAD_CACHE_E4M3;
+    const int nt = pl.token_tiles;
     if (cache->dim == 128)
-      rc = e4m3 ? launch_cache_token<128, kCacheE4m3>(p, ctas, st) : launch_cache_token<128, kCacheInt8>(p, ctas, st);
+      rc = e4m3 ? launch_cache_token<128, kCacheE4m3>(p, nt, ctas, st)
+                : launch_cache_token<128, kCacheInt8>(p, nt, ctas, st);
     else
-      rc = e4m3 ? launch_cache_token<64, kCacheE4m3>(p, ctas, st) : launch_cache_token<64, kCacheInt8>(p, ctas, st);
+      rc = e4m3 ? launch_cache_token<64, kCacheE4m3>(p, nt, ctas, st)
+                : launch_cache_token<64, kCacheInt8>(p, nt, ctas, st);
   } else {
     CUtensorMap mq = {}, mk = {}, mv = {};
     const int64_t any = cache->dim;   // stride of an axis of length one: any that the map takes

@@ -95,15 +95,15 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
 
-// 2^e as a bf16 pair, -127 <= e <= 127 (2^-127 is a subnormal)
+// 2^e as a bf16 pair, -126 <= e <= 127
 __device__ __forceinline__ uint32_t pow2_bf16x2(int e) {
-  const uint32_t b = e < -126 ? 0x40u : static_cast<uint32_t>(e + 127) << 7;
+  const uint32_t b = static_cast<uint32_t>(e + 127) << 7;
   return b | (b << 16);
 }
 
@@ -113,43 +113,52 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return r;
 }
 
-// Four stored bytes -> four bf16 numbers, before their scale.  e4m3: the seven
-// low bits moved to bf16's exponent and mantissa are the value times 2^-120
-// (subnormals included); one permute puts each byte in a high half, with the first
-// one's sign spread over the byte above it (selector bit 3), so that one
-// arithmetic shift by 4 carries both signs along and a mask clears the rest.
-// int8: 128 + the seven low bits is a bf16 number, and so is the 128 or 256 to
-// take from it.
+// A pair of bytes u in 0 .. 255, alone in the halves of `w`, -> (u - 128) / 128: as
+// bf16 bits u is the number u 2^-133 (the subnormals run into the normals), so one
+// exact multiply-add makes it u / 128 - 1.
+__device__ __forceinline__ uint32_t bytes_to_bf16x2(uint32_t w) { return fma_bf16x2(w, 0x7e807e80u, 0xbf80bf80u); }
+
+// Four stored bytes -> four bf16 numbers, before their scale: the value times
+// 2^-kUnpackBias.  e4m3: the seven low bits moved to bf16's exponent and mantissa
+// are the value times 2^-120 (subnormals included); one permute puts each byte in a
+// high half, with the first one's sign spread over the byte above it (selector bit
+// 3), so that one arithmetic shift by 4 carries both signs along and a mask clears
+// the rest.  int8: with the sign bit flipped the byte is the value + 128.
+template <int FMT>
+constexpr uint32_t kUnpackBias = FMT == kCacheE4m3 ? 120u : 7u;
+
 template <int FMT>
 __device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if (FMT == kCacheE4m3) {
     lo = static_cast<uint32_t>(static_cast<int32_t>(prmt(w, 0u, 0x1804u)) >> 4) & 0x87f087f0u;
     hi = static_cast<uint32_t>(static_cast<int32_t>(prmt(w, 0u, 0x3a24u)) >> 4) & 0x87f087f0u;
   } else {
-    const uint32_t a = prmt(w, 0x43434343u, 0x4140u), b = prmt(w, 0x43434343u, 0x4342u);
-    lo = sub_bf16x2(a & 0xff7fff7fu, a & 0xff80ff80u);
-    hi = sub_bf16x2(b & 0xff7fff7fu, b & 0xff80ff80u);
+    w ^= 0x80808080u;
+    lo = bytes_to_bf16x2(prmt(w, 0u, 0x4140u));
+    hi = bytes_to_bf16x2(prmt(w, 0u, 0x4342u));
   }
 }
 
 // Factors of a scale byte for what unpack4 gives.  The first alone does (and the
-// second is 1) but for scales over 2^7 of e4m3 pages, whose factor would leave
-// bf16's range.
+// second is 1) but for the NaN byte and scales whose factor would leave bf16's
+// range (over 2^7 for e4m3, 2^120 for int8).
 constexpr uint32_t kBf16One = 0x3f803f80u;
 
 template <int FMT>
+__device__ __forceinline__ bool odd_scale(uint32_t byte) {
+  return byte > 254u - kUnpackBias<FMT>;
+}
+
+template <int FMT>
 __device__ __forceinline__ void scale_factors(uint32_t byte, uint32_t& f1, uint32_t& f2) {
-  constexpr uint32_t kBias = FMT == kCacheE4m3 ? 120u : 0u;   // unpack4 gives e4m3 times 2^-120
-  f1 = (byte + kBias) * 0x00800080u;                          // the exponent field, twice
+  f1 = byte * 0x00800080u + kUnpackBias<FMT> * 0x00800080u;   // the exponent field, twice
   f2 = kBf16One;
-  if (byte + kBias - 1u > 253u) {
+  if (odd_scale<FMT>(byte)) {
     if (byte == kCacheNanScale) {
       f1 = 0x7fc07fc0u;
-    } else if (byte == 0u) {       // int8: 2^-127, a subnormal
-      f1 = 0x00400040u;
     } else {
       f1 = 0x7f007f00u;            // 2^127
-      f2 = pow2_bf16x2(static_cast<int>(byte + kBias) - 254);
+      f2 = pow2_bf16x2(static_cast<int>(byte + kUnpackBias<FMT>) - 254);
     }
   }
 }
@@ -165,7 +174,7 @@ __device__ __forceinline__ void dequant16(const uint4& w, uint32_t byte, uint4& 
   unpack4<FMT>(w.w, o1.z, o1.w);
   o0.x = mul_bf16x2(o0.x, f1); o0.y = mul_bf16x2(o0.y, f1); o0.z = mul_bf16x2(o0.z, f1); o0.w = mul_bf16x2(o0.w, f1);
   o1.x = mul_bf16x2(o1.x, f1); o1.y = mul_bf16x2(o1.y, f1); o1.z = mul_bf16x2(o1.z, f1); o1.w = mul_bf16x2(o1.w, f1);
-  if (FMT == kCacheE4m3 && f2 != kBf16One) {
+  if (f2 != kBf16One) {
     o0.x = mul_bf16x2(o0.x, f2); o0.y = mul_bf16x2(o0.y, f2); o0.z = mul_bf16x2(o0.z, f2); o0.w = mul_bf16x2(o0.w, f2);
     o1.x = mul_bf16x2(o1.x, f2); o1.y = mul_bf16x2(o1.y, f2); o1.z = mul_bf16x2(o1.z, f2); o1.w = mul_bf16x2(o1.w, f2);
   }
