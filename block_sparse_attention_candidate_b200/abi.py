@@ -552,27 +552,32 @@ class KVCache:
     written is never looked at)."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        if k.dim() != 4 or k.dtype not in CACHE_FORMATS or v.dtype != k.dtype or v.shape != k.shape:
+        shape, fmt = k.shape, CACHE_FORMATS.get(k.dtype)
+        if fmt is None or len(shape) != 4 or v.dtype != k.dtype or v.shape != shape:
             raise ValueError("k and v must be [num_pages, heads, page, dim] tensors of one shape, bf16, float8_e4m3fn "
                              "or int8")
-        if not (k.is_contiguous() and v.is_contiguous()):
-            raise ValueError("the pages must be contiguous")
-        pages, heads, page, dim = k.shape
-        fmt = CACHE_FORMATS[k.dtype]
+        pages, heads, page, dim = shape
+        dev = k.get_device()
+        same = k.is_contiguous() and v.is_contiguous() and v.get_device() == dev
+        ks = vs = None
         if fmt:
             want = (pages, heads, page, dim // CACHE_GROUP)
             for t in (k_scale, v_scale):
-                if t is None or t.dtype != torch.uint8 or t.shape != want or not t.is_contiguous():
+                if t is None or t.dtype != torch.uint8 or t.shape != want:
                     raise ValueError(f"an 8-bit cache needs contiguous uint8 k_scale and v_scale of shape {want}")
+                same = same and t.is_contiguous() and t.get_device() == dev
+            ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
         elif k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 cache has no scales")
-        for t in (v, k_scale, v_scale):
-            if t is not None and t.device != k.device:
-                raise ValueError("the cache's tensors must be on one device")
+        if not same:
+            raise ValueError("the cache's tensors must be contiguous and on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.heads, self.page, self.dim, self.device = heads, page, dim, k.device
-        self.c = DynradKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fmt else None,
-                               v_scale.data_ptr() if fmt else None, pages, heads, page, dim, fmt)
+        self.heads, self.page, self.dim, self.device_index = heads, page, dim, dev
+        self.c = DynradKvCache(k.data_ptr(), v.data_ptr(), ks, vs, pages, heads, page, dim, fmt)
+
+    @property
+    def device(self):
+        return self.k.device
 
     @classmethod
     def empty(cls, num_pages, heads, page, dim, dtype=torch.bfloat16, device=None):
@@ -587,46 +592,54 @@ class KVCache:
 def _cache_seqs(cache, page_table, cu_seq, kv_len, num_tokens) -> DynradSeqs:
     """The C struct of a call's sequences, after host checks that keep the
     kernels inside the tensors.  Raises ValueError."""
-    if page_table.dim() != 2 or cu_seq.dim() != 1 or kv_len.dim() != 1:
+    if page_table.dim() != 2:
         raise ValueError("page_table is [S, max_pages], cu_seq [S + 1], kv_len [S]")
     S, cols = page_table.shape
-    if page_table.dtype != torch.int32 or cu_seq.dtype != torch.int32 or kv_len.dtype != torch.int32:
+    i32, dev = torch.int32, cache.device_index
+    if page_table.dtype != i32 or cu_seq.dtype != i32 or kv_len.dtype != i32:
         raise ValueError("page_table, cu_seq and kv_len must be int32 tensors")
-    if cu_seq.shape[0] != S + 1 or kv_len.shape[0] != S:
+    if cu_seq.shape != (S + 1,) or kv_len.shape != (S,):
         raise ValueError(f"page_table has {S} rows: cu_seq needs {S + 1} entries and kv_len {S}")
-    if not (cu_seq.is_contiguous() and kv_len.is_contiguous()) or (cols > 1 and page_table.stride(1) != 1):
-        raise ValueError("cu_seq and kv_len must be contiguous, page_table in its rows")
-    if page_table.device != cache.device or cu_seq.device != cache.device or kv_len.device != cache.device:
+    if page_table.get_device() != dev or cu_seq.get_device() != dev or kv_len.get_device() != dev:
         raise ValueError("page_table, cu_seq and kv_len must be on the cache's device")
-    stride = page_table.stride(0) if S > 1 else cols
-    if stride < cols:
-        raise ValueError("page_table's rows must not overlap")
+    stride, col = page_table.stride()
+    if S <= 1:
+        stride = cols
+    if stride < cols or (cols > 1 and col != 1) or not cu_seq.is_contiguous() or not kv_len.is_contiguous():
+        raise ValueError("cu_seq and kv_len must be contiguous, page_table in its rows, which must not overlap")
     return DynradSeqs(page_table.data_ptr(), cu_seq.data_ptr(), kv_len.data_ptr(), stride, S, cols, num_tokens)
 
 
 def _cache_rows(cache, name, t, heads, tokens=None, head_major=False, written=False):
     """(token stride, head stride) of a bf16 [T, heads, D] tensor ([heads, T, D]
     with head_major) whose rows the kernels move 16 bytes at a time."""
-    ti, hi = (1, 0) if head_major else (0, 1)
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.shape[2] != cache.dim or t.shape[hi] != heads or (
-            tokens is not None and t.shape[ti] != tokens):
-        raise ValueError(f"{name} must be bf16 [{'heads, T' if head_major else 'T, heads'}, {cache.dim}] with "
-                         f"{heads} heads" + ("" if tokens is None else f" and {tokens} tokens"))
-    if t.device != cache.device:
+    dim = cache.dim
+    if t.dim() != 3 or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bf16 tensor of three dimensions")
+    if head_major:
+        (H, T, D), (hs, ts, ds) = t.shape, t.stride()
+    else:
+        (T, H, D), (ts, hs, ds) = t.shape, t.stride()
+    if D != dim or H != heads or (tokens is not None and T != tokens):
+        raise ValueError(f"{name} must be [{'heads, T' if head_major else 'T, heads'}, {dim}] with {heads} heads" +
+                         ("" if tokens is None else f" and {tokens} tokens"))
+    if t.get_device() != cache.device_index:
         raise ValueError(f"{name} must be on the cache's device")
-    ts = t.stride(ti) if t.shape[ti] > 1 else heads * cache.dim
-    hs = t.stride(hi) if heads > 1 else cache.dim
-    if t.stride(2) != 1 or ts % 8 or hs % 8 or ts < 0 or hs < 0:
+    if T <= 1:
+        ts = heads * dim
+    if heads <= 1:
+        hs = dim
+    if ds != 1 or ts % 8 or hs % 8 or ts < 0 or hs < 0:
         raise ValueError(f"{name}: the last dimension must be contiguous and the strides multiples of 8 elements")
-    if written and t.numel():
-        a, b = sorted(((ts, t.shape[ti]), (hs, heads)))
-        if (a[1] > 1 and a[0] < cache.dim) or (b[1] > 1 and b[0] < a[0] * (a[1] - 1) + cache.dim):
+    if written and T:
+        a, b = ((ts, T), (hs, heads)) if ts <= hs else ((hs, heads), (ts, T))
+        if (a[1] > 1 and a[0] < dim) or (b[1] > 1 and b[0] < a[0] * (a[1] - 1) + dim):
             raise ValueError(f"{name} is written: its rows must not overlap")
     return ts, hs
 
 
 def _require_current(cache):
-    if cache.device.type != "cuda" or cache.device.index != torch.cuda.current_device():
+    if cache.device_index < 0 or cache.device_index != torch.cuda.current_device():
         raise ValueError("the cache must be on the current CUDA device")
 
 

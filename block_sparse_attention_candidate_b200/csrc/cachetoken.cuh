@@ -79,10 +79,10 @@ template <int FMT, int K>
 __device__ __forceinline__ uint32_t unpack_pair(uint32_t a, uint32_t b, uint32_t flip) {
   if (FMT == kCacheE4m3) {
     constexpr uint32_t kSel = ((4u + K) << 12) | ((8u | K) << 8) | (K << 4) | K;
-    return static_cast<uint32_t>(static_cast<int32_t>(prmt(a, b, kSel)) >> 4) & 0x87f087f0u;
+    return static_cast<uint32_t>(static_cast<int32_t>(prmt<kSel>(a, b)) >> 4) & 0x87f087f0u;
   }
   constexpr uint32_t kSel = ((4u + K) << 12) | ((4u + K) << 8) | (K << 4) | K;
-  return bytes_to_bf16x2((prmt(a, b, kSel) & 0x00ff00ffu) ^ flip);
+  return bytes_to_bf16x2((prmt<kSel>(a, b) & 0x00ff00ffu) ^ flip);
 }
 
 // What a thread carries through its warp's blocks of a segment.
@@ -224,8 +224,8 @@ __device__ __forceinline__ void token_block(TokenState<D, NT>& me, const uint8_t
 #pragma unroll
     for (int i = 0; i < 4; ++i) scale_factors<FMT>(vbyte[i], f1[i], f2[i]);
   }
-  const uint32_t fa = prmt(f1[0], f1[1], 0x5410u), fb = prmt(f1[2], f1[3], 0x5410u);
-  const uint32_t ga = prmt(f2[0], f2[1], 0x5410u), gb = prmt(f2[2], f2[3], 0x5410u);
+  const uint32_t fa = prmt<0x5410u>(f1[0], f1[1]), fb = prmt<0x5410u>(f1[2], f1[3]);
+  const uint32_t ga = prmt<0x5410u>(f2[0], f2[1]), gb = prmt<0x5410u>(f2[2], f2[3]);
 #pragma unroll
   for (int w = 0; w < VB / 4; ++w) {
     uint32_t a[4] = {unpack_pair<FMT, 0>(x[0][w], x[1][w], me.flip), unpack_pair<FMT, 1>(x[0][w], x[1][w], me.flip),

@@ -107,9 +107,12 @@ __device__ __forceinline__ uint32_t pow2_bf16x2(int e) {
   return b | (b << 16);
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+// Bytes of a (0 .. 3) and b (4 .. 7) by the selector's four-bit fields; bit 3 of a
+// field spreads the byte's sign instead.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "n"(SEL));
   return r;
 }
 
@@ -130,12 +133,12 @@ constexpr uint32_t kUnpackBias = FMT == kCacheE4m3 ? 120u : 7u;
 template <int FMT>
 __device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if (FMT == kCacheE4m3) {
-    lo = static_cast<uint32_t>(static_cast<int32_t>(prmt(w, 0u, 0x1804u)) >> 4) & 0x87f087f0u;
-    hi = static_cast<uint32_t>(static_cast<int32_t>(prmt(w, 0u, 0x3a24u)) >> 4) & 0x87f087f0u;
+    lo = static_cast<uint32_t>(static_cast<int32_t>(prmt<0x1804u>(w, 0u)) >> 4) & 0x87f087f0u;
+    hi = static_cast<uint32_t>(static_cast<int32_t>(prmt<0x3a24u>(w, 0u)) >> 4) & 0x87f087f0u;
   } else {
     w ^= 0x80808080u;
-    lo = bytes_to_bf16x2(prmt(w, 0u, 0x4140u));
-    hi = bytes_to_bf16x2(prmt(w, 0u, 0x4342u));
+    lo = bytes_to_bf16x2(prmt<0x4140u>(w, 0u));
+    hi = bytes_to_bf16x2(prmt<0x4342u>(w, 0u));
   }
 }
 
