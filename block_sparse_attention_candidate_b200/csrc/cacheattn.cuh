@@ -33,7 +33,8 @@
 //              over the first half of S.
 //   warp 8     producer: publishes the segments (an item or a part of it), loads
 //              Q by TMA (a [D, heads, tokens] map: any strides) and each step's K
-//              and V pages, one lane a page.
+//              pages, one lane a page;
+//   warp 10    the same for V's pages.
 //   warp 9     MMA issuer: O_t += P_t V(j), then S_t = Q_t K(j+1)^T.
 //   warps 12-19 (8-bit pages) turn what was loaded into bf16 operand tiles.
 //              Scales are powers of two, so those tiles are exact and everything
@@ -42,9 +43,10 @@
 // What nobody sees.  A masked logit is replaced, not added to, so K may hold
 // anything.  V meets P = 0 in the product, where NaN and infinity would not
 // stay away: on steps that some row of the item does not see whole (`partial`),
-// V rows outside [lo, hi) of the item are zeroed in shared memory, and channels
-// inside it that are not finite are zeroed too and noted (`poison`); the epilogue of
-// a poisoned segment adds those back, in the rows that do see them, by plain loads.
+// V rows that no row sees are zeroed in shared memory, and of those that some but not
+// all rows see the channels that are not finite are zeroed too and noted (`poison`);
+// the epilogue of a poisoned segment adds those back, in the rows that do see them,
+// by plain loads.
 //
 // Every wait is bounded (common.cuh).
 #pragma once
@@ -73,11 +75,11 @@ struct CacheAttnCfg {
   static constexpr int kRawFit = kRaw ? (kBudget - kSlots * kTileBytes) / kRawBytes : 0;
   static constexpr int kRawSlots = kRawFit < 8 ? kRawFit : 8;
   static constexpr int kDqWarps = kRaw ? 8 : 0;
-  static constexpr int kThreads = kRaw ? 640 : 320;
+  static constexpr int kThreads = kRaw ? 640 : 352;
   // 8-bit: registers a thread after the split by warpgroup (two of softmax, one of
   // producer and MMA, two that dequantise); 640 threads start with 96
-  static constexpr int kRegsSoftmax = 144, kRegsOther = 64;
-  static_assert(256 * kRegsSoftmax + 384 * kRegsOther <= 640 * 96, "registers at launch");
+  static constexpr int kRegsSoftmax = 144, kRegsControl = 64, kRegsUnpack = 64;
+  static_assert(256 * kRegsSoftmax + 128 * kRegsControl + 256 * kRegsUnpack <= 640 * 96, "registers at launch");
   static constexpr int kSmem = QT * kTileBytes + kSlots * kTileBytes + kRawSlots * kRawBytes + kCtrl + 1024;
   static constexpr int kRows = 128 * QT;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
     }
     for (int g = 0; g < kSegRing; ++g) {
       mbar_init(&seg_full[g], 1);
-      mbar_init(&seg_empty[g], 9 + C::kDqWarps);   // softmax, MMA and dequantising warps
+      mbar_init(&seg_empty[g], 10 + C::kDqWarps);   // softmax, MMA, V's producer and dequantising warps
       poison[g] = 0;
     }
     mbar_init(ml_full, 4);
@@ -353,6 +355,78 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
 
   // waits for segment g of the CTA and gives it back when a warp is through with it
   auto seg_wait = [&](int g) -> bool { return mbar_wait(&seg_full[g % kSegRing], (g / kSegRing) & 1, abort_flag, wlim); };
+
+  // The K (kv = 0) or V tiles of the sequence's steps [step_a, step_b), as loads li, li + 2, ..; lane b has page b
+  // of a step.  A producer's pages go out one lane after the other (some 60 clocks a
+  // copy), so K and V have a warp each.
+  const int ps = p.c.page_shift, page = 1 << ps, npg = 128 >> ps;
+  auto load_tiles = [&](int kv, int seq, int head, int step_a, int step_b, int32_t lo, int32_t hi, int& li) -> bool {
+    const int32_t* row = p.s.page_table + static_cast<int64_t>(seq) * p.s.table_stride;
+    // page of lane's positions of step j: -1 not needed, -2 outside the pool
+    auto page_of = [&](int j) -> int32_t {
+      const int64_t key = (static_cast<int64_t>(j) << 7) + (lane << ps);
+      if (lane >= npg || key >= hi || key + page <= lo) return -1;
+      const int32_t pg = row[key >> ps];
+      if (pg >= 0 && pg < p.c.num_pages) return pg;
+      record_error(DYNRAD_ERR_DEVICE);
+      return -2;
+    };
+    int32_t pg = step_a < step_b ? page_of(step_a) : -1;
+    for (int j = step_a; j < step_b; ++j, li += 2) {
+      const int32_t next = j + 1 < step_b ? page_of(j + 1) : -1;
+      const int pages = __popc(__ballot_sync(0xffffffffu, C::kRaw ? pg >= 0 : pg != -1));
+      const int64_t tile = (static_cast<int64_t>(pg) * p.c.heads + head) << ps;   // first row of the page's head
+      constexpr int n = C::kRaw ? NR : NS;
+      const int sl = li % n;
+      uint64_t* full = C::kRaw ? &raw_full[sl] : &slot_full[sl];
+      uint64_t* empty = C::kRaw ? &raw_empty[sl] : &slot_empty[sl];
+      bool w = true;
+      if (li >= n && lane == 0) w = mbar_wait(empty, ((li / n) - 1) & 1, abort_flag, wlim);
+      if (!__shfl_sync(0xffffffffu, w, 0)) return false;
+      if constexpr (C::kRaw) {
+        uint8_t* dst = raw_smem + sl * C::kRawBytes;
+        if (pg == -2) {   // reads as zeros
+          for (int i = 0; i < page * D / 16; ++i)
+            reinterpret_cast<uint4*>(dst + (lane << ps) * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < page * (D / kCacheGroup); ++i)
+            dst[C::kRawCodes + (lane << ps) * (D / kCacheGroup) + i] = 127;
+          fence_async_shared();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(full, pages * page * (D + D / kCacheGroup));
+        __syncwarp();
+        if (pg >= 0) {
+          const uint8_t* codes = kv == 0 ? p.c.k : p.c.v;
+          const uint8_t* scales = kv == 0 ? p.c.k_scale : p.c.v_scale;
+          bulk_load(dst + (lane << ps) * D, codes + tile * D, page * D, full);
+          bulk_load(dst + C::kRawCodes + (lane << ps) * (D / kCacheGroup), scales + tile * (D / kCacheGroup),
+                    page * (D / kCacheGroup), full);
+        }
+      } else {
+        uint8_t* dst = slot_smem + sl * TB;
+        if (lane == 0) mbar_arrive_expect_tx(full, pages * page * D * 2);
+        __syncwarp();
+        if (pg != -1) {
+          // a row past the tensor (a page outside the pool) is filled with zeros
+          const int32_t r = static_cast<int32_t>(pg >= 0 ? tile : (p.c.num_pages * p.c.heads) << ps);
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_2d(dst + c * C::kChunkBytes + (lane << ps) * 128, kv == 0 ? &tm_k : &tm_v, full, c * 64, r);
+        }
+      }
+      __syncwarp();
+      pg = next;
+    }
+    return true;
+  };
+  // unwinding: lets the copies of loads li - 2, li - 4, .. land before shared memory is
+  // given back
+  auto drain_loads = [&](int li) {
+    constexpr int n = C::kRaw ? NR : NS;
+    if (lane == 0)
+      for (int i = li - 2; i >= 0 && i > li - 2 - n; i -= 2)
+        mbar_wait(C::kRaw ? &raw_full[i % n] : &slot_full[i % n], (i / n) & 1, nullptr);
+  };
 
   if (warp < 8) {
     if constexpr (C::kRaw) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
@@ -387,20 +461,23 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
         ++ns;
         tc_fence_after();
         if (!C::kRaw && tile == 0 && seg_partial(sg, j)) {
-          // thread = key: V rows that nobody sees, or that are not finite
           if (!__all_sync(0xffffffffu,
                           mbar_wait(&slot_full[(li + 1) % NS], ((li + 1) / NS) & 1, abort_flag, wlim))) {
             ok = false;
             break;
           }
-          uint8_t* vrow = slot_smem + ((li + 1) % NS) * TB + t * 128;
-          const bool seen = key0 + t >= sg.it.lo && key0 + t < sg.it.hi;
+          // eight lanes a row: V rows that nobody sees, and of those that some rows see
+          // what is not finite
           bool bad = false;
+#pragma unroll 1
+          for (int r = warp * 32 + (lane >> 3); r < warp * 32 + 32; r += 4) {
+            const int32_t key = key0 + r;
+            if (key >= sg.it.lo_max && key < sg.it.hi_min) continue;     // seen by all
+            const bool seen = key >= sg.it.lo && key < sg.it.hi;
 #pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              uint4* at = reinterpret_cast<uint4*>(vrow + c * C::kChunkBytes + u * 16);
+            for (int c = 0; c < C::kChunks; ++c) {
+              uint4* at = reinterpret_cast<uint4*>(slot_smem + ((li + 1) % NS) * TB + c * C::kChunkBytes + r * 128 +
+                                                   (lane & 7) * 16);
               uint4 y = make_uint4(0u, 0u, 0u, 0u);
               if (seen) {
                 const uint4 x = *at;
@@ -410,6 +487,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
               }
               *at = y;
             }
+          }
           if (bad) poison[g % kSegRing] = g + 1;
           fence_async_shared();
         }
@@ -426,28 +504,41 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
 #pragma unroll kHalves
           for (int h = 0; h < 2; ++h) {
             if ((half_none >> h) & 1u) continue;
-            float sv[64];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t r[32];
-              tmem_ld32(taddr + lane_base + col_s + h * 64 + c * 32, r);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(r[i]);
-            }
-            tmem_wait_ld();
+            float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
             if ((half_full >> h) & 1u) {
-              float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+              float sv[64];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint32_t r[32];
+                tmem_ld32(taddr + lane_base + col_s + h * 64 + c * 32, r);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(r[i]);
+              }
+              tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 64; i += 8) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) m4[u] = fmax3(m4[u], sv[i + 2 * u], sv[i + 2 * u + 1]);
               }
-              mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
             } else {
+              // columns that do not count become -inf, in tensor memory too: the second
+              // pass takes all it reads
+#pragma unroll kHalves
+              for (int c = h * 64; c < h * 64 + 64; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(taddr + lane_base + col_s + c, r);
+                tmem_wait_ld();
+                const int from = rl - c, to = rh - c;
 #pragma unroll
-              for (int i = 0; i < 64; ++i)
-                if (h * 64 + i >= rl && h * 64 + i < rh) mx = fmaxf(mx, sv[i]);
+                for (int i = 0; i < 32; ++i) {
+                  if (i < from || i >= to) r[i] = 0xff800000u;
+                  m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(r[i]));
+                }
+                tmem_st32(taddr + lane_base + col_s + c, r);
+              }
+              tmem_wait_st();
             }
+            mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
           }
           const float m_new = fmaxf(m_used, mx * c2);
           const bool need = valid && m_used != -INFINITY && m_new > m_used + 8.0f;
@@ -488,11 +579,6 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
                 for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(r[i]);
               }
               tmem_wait_ld();
-              if (!((half_full >> h) & 1u)) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                  if (h * 64 + i < rl || h * 64 + i >= rh) sv[i] = -INFINITY;
-              }
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float2 x = __ffma2_rn(make_float2(sv[2 * i], sv[2 * i + 1]), cc, mm);
@@ -577,6 +663,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
               if (!seg_partial(sg, j)) continue;
               const int32_t key0 = (step0 + j) << 7;
               for (int32_t key = max(lo, key0); key < min(hi, key0 + 128); ++key) {
+                if (key >= sg.it.lo_max && key < sg.it.hi_min) continue;
                 const int64_t at = cache_row(p.c, p.s, sg.it.seq, key);
                 if (at < 0) continue;
                 const int64_t row = at + (static_cast<int64_t>(sg.head) << p.c.page_shift);
@@ -627,11 +714,10 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
         mbar_arrive(&seg_empty[g % kSegRing]);
       }
     }
-  } else {
-    if constexpr (C::kRaw) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+  } else if (warp < 12) {   // 11 only fills up the warpgroup
+    if constexpr (C::kRaw) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsControl));
   if (warp == 8) {
     // ------------------------------------------------------------- producer
-    const int ps = p.c.page_shift, page = 1 << ps, npg = 128 >> ps;
     int head = 0, place = 0;
     int64_t off = 0, left = 0;
     if (p.split) {
@@ -655,7 +741,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
       }
     }
     bool ok = true;
-    int g = 0, nq = 0, li = 0;   // segments, Q loads, K / V tile loads
+    int g = 0, nq = 0, li = 0;   // segments, Q loads, K tile loads (even numbers)
     auto publish = [&](const CacheSeg& sg) -> bool {
       bool w = true;
       if (g >= kSegRing && lane == 0)
@@ -726,68 +812,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
                             sg.it.tok0 + t * p.tile_tokens);
           }
           ++nq;
-          // K and V of each step; lane b < npg has page b of the step
-          const int32_t* row = p.s.page_table + static_cast<int64_t>(sg.it.seq) * p.s.table_stride;
-          // page of lane's positions of step j: -1 not needed, -2 outside the pool
-          auto page_of = [&](int j) -> int32_t {
-            const int64_t key = (static_cast<int64_t>(sg.it.step0 + j) << 7) + (lane << ps);
-            if (lane >= npg || key >= sg.it.hi || key + page <= sg.it.lo) return -1;
-            const int32_t pg = row[key >> ps];
-            if (pg >= 0 && pg < p.c.num_pages) return pg;
-            record_error(DYNRAD_ERR_DEVICE);
-            return -2;
-          };
-          int32_t pg = page_of(sg.sa);
-          for (int j = sg.sa; ok && j < sg.sb; ++j) {
-            const int32_t next = j + 1 < sg.sb ? page_of(j + 1) : -1;
-            const int pages = __popc(__ballot_sync(0xffffffffu, C::kRaw ? pg >= 0 : pg != -1));
-            const int64_t tile = (static_cast<int64_t>(pg) * p.c.heads + head) << ps;   // first row of the page's head
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-              const int sl = C::kRaw ? li % NR : li % NS;
-              uint64_t* full = C::kRaw ? &raw_full[sl] : &slot_full[sl];
-              uint64_t* empty = C::kRaw ? &raw_empty[sl] : &slot_empty[sl];
-              const int n = C::kRaw ? NR : NS;
-              w = true;
-              if (li >= n && lane == 0) w = mbar_wait(empty, ((li / n) - 1) & 1, abort_flag, wlim);
-              if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
-              if (C::kRaw) {
-                uint8_t* dst = raw_smem + sl * C::kRawBytes;
-                if (pg == -2) {   // reads as zeros
-                  for (int i = 0; i < page * D / 16; ++i)
-                    reinterpret_cast<uint4*>(dst + (lane << ps) * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-                  for (int i = 0; i < page * (D / kCacheGroup); ++i)
-                    dst[C::kRawCodes + (lane << ps) * (D / kCacheGroup) + i] = 127;
-                  fence_async_shared();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(full, pages * page * (D + D / kCacheGroup));
-                __syncwarp();
-                if (pg >= 0) {
-                  const uint8_t* codes = kv == 0 ? p.c.k : p.c.v;
-                  const uint8_t* scales = kv == 0 ? p.c.k_scale : p.c.v_scale;
-                  bulk_load(dst + (lane << ps) * D, codes + tile * D, page * D, full);
-                  bulk_load(dst + C::kRawCodes + (lane << ps) * (D / kCacheGroup),
-                            scales + tile * (D / kCacheGroup), page * (D / kCacheGroup), full);
-                }
-              } else {
-                uint8_t* dst = slot_smem + sl * TB;
-                if (lane == 0) mbar_arrive_expect_tx(full, pages * page * D * 2);
-                __syncwarp();
-                if (pg != -1) {
-                  // a row past the tensor (a page outside the pool) is filled with zeros
-                  const int32_t r = static_cast<int32_t>(
-                      pg >= 0 ? tile : (p.c.num_pages * p.c.heads) << ps);
-#pragma unroll
-                  for (int c = 0; c < C::kChunks; ++c)
-                    tma_load_2d(dst + c * C::kChunkBytes + (lane << ps) * 128, kv == 0 ? &tm_k : &tm_v, full, c * 64, r);
-                }
-              }
-              __syncwarp();
-              ++li;
-            }
-            pg = next;
-          }
+          ok = load_tiles(0, sg.it.seq, head, sg.it.step0 + sg.sa, sg.it.step0 + sg.sb, sg.it.lo, sg.it.hi, li);
         }
       }
       ++place;
@@ -800,12 +825,9 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
       sg.end = 1;
       ok = publish(sg);
     }
-    if (!ok && lane == 0) {
-      // unwinding: let the copies already issued land before shared memory is given back
-      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1, nullptr);
-      const int n = C::kRaw ? NR : NS;
-      for (int i = (li > n ? li - n : 0); i < li; ++i)
-        mbar_wait(C::kRaw ? &raw_full[i % n] : &slot_full[i % n], (i / n) & 1, nullptr);
+    if (!ok) {
+      if (nq > 0 && lane == 0) mbar_wait(q_full, (nq - 1) & 1, nullptr);
+      drain_loads(li);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -926,9 +948,28 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
     commit(drain);
     mbar_wait(drain, 0, nullptr);
     __syncwarp();
-  } else if (warp >= 12) {   // 10 and 11 only fill up the third warpgroup
+  } else if (warp == 10) {
+    // ----------------------------------------------------------- V's producer
+    int li = 1;
+    bool ok = true;
+    for (int g = 0; ok; ++g) {
+      if (!__all_sync(0xffffffffu, seg_wait(g))) { ok = false; break; }
+      const CacheSeg& sr = segs[g % kSegRing];
+      const int seq = sr.it.seq, head = sr.head, a = sr.it.step0 + sr.sa, b = sr.it.step0 + sr.sb;
+      const int32_t lo = sr.it.lo, hi = sr.it.hi;
+      const bool end = sr.end;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[g % kSegRing]);
+      if (end) break;
+      ok = load_tiles(1, seq, head, a, b, lo, hi, li);
+    }
+    if (!ok) drain_loads(li);
+    __syncwarp();
+  }
+  } else {
     // -------------------------------------------------- 8-bit pages to bf16 tiles
     if constexpr (C::kRaw) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsUnpack));
       constexpr int U = D / 16;                          // 16-channel units a row
       constexpr int RP = C::kDqWarps * 32 / U;           // rows a pass, a multiple of 8
       constexpr int NP = 128 / RP;
@@ -976,7 +1017,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
               for (int i = 0; i < NP; ++i) {
                 const int key = key0 + r0 + i * RP;
                 const bool seen = key >= lo && key < hi;
-                if (!seen || byte[i] == kCacheNanScale) {
+                const bool all = key >= lo_max && key < hi_min;
+                if (!seen || (byte[i] == kCacheNanScale && !all)) {
                   bad = bad || seen;
                   x[i] = make_uint4(0u, 0u, 0u, 0u);
                   byte[i] = 127;
@@ -1007,7 +1049,6 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
       }
     }
   }
-  }
 
   tc_fence_before();
   __syncthreads();
@@ -1017,12 +1058,20 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
 
 // Joins the parts of the items that a split launch cut: CTA x has the item whose
 // first part CTA x of that launch wrote (slot 1), followed by slot 0 of the CTAs
-// after it up to the last part.  Weights 2^(m_i - max m) in order of the parts.
+// after it up to the last part.  Weights 2^(m_i - max m), sums in order of the parts.
+// A row belongs to D / 4 lanes: they weigh its parts side by side, then each adds up
+// its four channels, eight parts' loads in flight (74 parts of 8 rows: 21 -> 6 us
+// against one part after the other).
+constexpr int kJoinThreads = 256;
+constexpr int kJoinMost = 3 * kCacheMaxCtas;     // parts of an item, at most one for each CTA
+
 template <int D>
-__global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p, int item_tokens, int rows_per_part,
-                                                         int ctas) {
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAttnParams p, int item_tokens,
+                                                                  int rows_per_part, int ctas) {
+  constexpr int L = D / 4;        // lanes a row
+  constexpr int R = kJoinThreads / L;
+  __shared__ float weights[R][kJoinMost];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int L = D / 4;        // threads a row
   const int x = blockIdx.x;
   const int4 d0 = p.part_desc[2 * x + 1];
   if (d0.z != kPartOpen) return;
@@ -1035,25 +1084,48 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
   }
   const CacheItem it = find_item(p, item_tokens, d0.x);
   // row = tile * 128 + token of the tile * group + head of the group
-  const int tile_rows = p.tile_tokens * p.group;
-  const int c = threadIdx.x % L;
-  for (int i = blockIdx.y * (256 / L) + threadIdx.x / L; i < it.ntok * p.group; i += gridDim.y * (256 / L)) {
+  const int tile_rows = p.tile_tokens * p.group, rows = it.ntok * p.group;
+  const int c = threadIdx.x % L, slot = threadIdx.x / L;
+  const uint32_t lanes = L == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
+  float* w = weights[slot];
+  for (int i = blockIdx.y * R + slot; i < rows; i += gridDim.y * R) {
     const int tile = i / tile_rows, row = tile * 128 + (i - tile * tile_rows);
     auto at = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * x + 1 : 2 * (x + k)) * rows_per_part + row; };
+    // the first eight parts' channels do not wait for the weights
+    float4 v[8];
+    auto fetch = [&](int k0) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (k0 + u < parts) v[u] = __ldcs(reinterpret_cast<const float4*>(p.part_o + at(k0 + u) * D) + c);
+    };
+    fetch(0);
     float m = -INFINITY, l = 0.f;
-    for (int k = 0; k < parts; ++k) m = fmaxf(m, p.part_ml[at(k)].x);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < parts; ++k) {
+    for (int k = c; k < parts; k += L) m = fmaxf(m, p.part_ml[at(k)].x);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
+    for (int k = c; k < parts; k += L) {
       const float2 b = p.part_ml[at(k)];
-      const float w = b.x == -INFINITY ? (b.y == 0.f ? 0.f : 1.f) : ex2_approx(b.x - m);
-      if (w == 0.f) continue;
-      const float4 v = reinterpret_cast<const float4*>(p.part_o + at(k) * D)[c];
-      l = fmaf(b.y, w, l);
-      o.x = fmaf(v.x, w, o.x);
-      o.y = fmaf(v.y, w, o.y);
-      o.z = fmaf(v.z, w, o.z);
-      o.w = fmaf(v.w, w, o.w);
+      const float f = b.x == -INFINITY ? (b.y == 0.f ? 0.f : 1.f) : ex2_approx(b.x - m);
+      w[k] = f;
+      l = f == 0.f ? l : fmaf(b.y, f, l);
     }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) l += __shfl_xor_sync(lanes, l, o);
+    __syncwarp(lanes);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < parts; k0 += 8) {
+      if (k0 > 0) fetch(k0);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float f = k0 + u < parts ? w[k0 + u] : 0.f;
+        if (f == 0.f) continue;
+        o.x = fmaf(v[u].x, f, o.x);
+        o.y = fmaf(v[u].y, f, o.y);
+        o.z = fmaf(v[u].z, f, o.z);
+        o.w = fmaf(v[u].w, f, o.w);
+      }
+    }
+    __syncwarp(lanes);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t token = it.tok0 + i / p.group;
     const int head = d0.y * p.group + i % p.group;

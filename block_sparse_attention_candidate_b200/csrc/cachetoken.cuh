@@ -96,11 +96,12 @@ struct TokenState {
 };
 
 // One block of 16 keys from key0 on, its bytes at st.  partial: some row of the item,
-// which sees [lo, hi), does not see all of it.  odd: some scale's factor takes more
+// which sees [lo, hi) and every row of it [lo_max, hi_min), does not see all of it.  odd: some scale's factor takes more
 // than a shift of its byte (odd_scale); such blocks are rare.
 template <int D, int FMT, int NT>
 __device__ __forceinline__ void token_block(TokenState<D, NT>& me, const uint8_t* st, int key0, bool partial, bool odd,
-                                            int32_t lo, int32_t hi, float scale_log2, const uint32_t (&kbyte)[2][D / 64],
+                                            int32_t lo, int32_t hi, int32_t lo_max, int32_t hi_min, float scale_log2,
+                                            const uint32_t (&kbyte)[2][D / 64],
                                             uint32_t (&vbyte)[4], const uint2* qs, volatile int* poison) {
   constexpr int KW = D / 64, VB = D / 8, NJ = D / 16;
   using C = CacheTokenCfg<D, NT>;
@@ -209,7 +210,7 @@ __device__ __forceinline__ void token_block(TokenState<D, NT>& me, const uint8_t
     for (int i = 0; i < 4; ++i) {
       const int key = key0 + t + 4 * i;
       const bool seen = key >= lo && key < hi;
-      if (!seen || vbyte[i] == kCacheNanScale) {
+      if (!seen || (vbyte[i] == kCacheNanScale && (key < lo_max || key >= hi_min))) {
         if (seen) *poison = 1;
         vbyte[i] = 127;
 #pragma unroll
@@ -453,8 +454,8 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
         vbyte[i] = st[vs_off + i * 4 * (D / kCacheGroup)];
         odd = odd || odd_scale<FMT>(vbyte[i]);
       }
-      token_block<D, FMT, NT>(me, st, key0, partial, __any_sync(0xffffffffu, odd), it.lo, it.hi, p.scale_log2, kbyte,
-                              vbyte, q_s + lane, poison);
+      token_block<D, FMT, NT>(me, st, key0, partial, __any_sync(0xffffffffu, odd), it.lo, it.hi, it.lo_max,
+                              it.hi_min, p.scale_log2, kbyte, vbyte, q_s + lane, poison);
       __syncwarp();      // every lane has read the stage
       load(b + C::kStages * kTokenWarps, next_page, stage);
       next_page = page_of(b + (C::kStages + 1) * kTokenWarps);
@@ -504,8 +505,7 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
         seen_range(p.frame, p.window, it.pos0 + tok, it.len, lo, hi);
         const int first = max(lo, static_cast<int>(ka)), last = min(static_cast<int64_t>(hi), kb);
         for (int key = first; key < last; ++key) {
-          const int k0 = key & ~15;
-          if (!(k0 < it.lo_max || k0 > it.hi_min - 16)) continue;
+          if (key >= it.lo_max && key < it.hi_min) continue;
           const int64_t at = cache_row(p.c, p.s, it.seq, key);
           if (at >= 0 && p.c.v_scale[(at + (static_cast<int64_t>(kvh) << ps)) * (D / kCacheGroup) + c * 4 / kCacheGroup] ==
                              kCacheNanScale)

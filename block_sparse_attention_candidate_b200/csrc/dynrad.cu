@@ -1234,8 +1234,11 @@ struct CachePlan {
 };
 
 constexpr int kCacheMaxPlan = 2048;   // places a CTA scans at its start
+constexpr int kCacheShort = 1024;     // keys that one CTA goes through sooner than two launches take
 
-int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, int32_t heads, CachePlan* pl) {
+// max_keys: what a sequence can hold (its row of the page table).
+int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, int32_t heads, int64_t max_keys,
+               CachePlan* pl) {
   if (heads < 1 || c->heads < 1 || heads % c->heads != 0) return DYNRAD_ERR_INVALID_ARG;
   pl->group = heads / c->heads;
   if (pl->group > 128) return DYNRAD_ERR_UNSUPPORTED;
@@ -1258,11 +1261,12 @@ int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, i
   if (slots > INT32_MAX || c->heads > 65535) return DYNRAD_ERR_UNSUPPORTED;
   pl->slots = static_cast<int32_t>(slots);
   // The even cut pays while items are few or single sequences may be most of the
-  // work; full items in many waves leave little to even out, and keep a head's
-  // keys in L2 when they run head after head.
+  // work.  Full items in many waves leave little to even out, and keep a head's
+  // keys in L2 when they run head after head; with few keys an item is done before
+  // the parts could be joined.
   const bool many = slots * c->heads >= 8 * kCacheMaxCtas &&
                     static_cast<int64_t>(num_tokens) >= static_cast<int64_t>(num_seqs) * pl->item_tokens;
-  pl->split = slots <= kCacheMaxPlan && !many;
+  pl->split = slots <= kCacheMaxPlan && !many && max_keys > kCacheShort;
   const size_t ctas = static_cast<size_t>(kCacheMaxCtas) * pl->ctas_per_sm, rows = 2 * ctas * pl->part_rows;
   pl->part_ml = pl->split ? align256(rows * c->dim * 4) : 0;
   pl->part_desc = pl->split ? align256(pl->part_ml + rows * 8) : 0;
@@ -1329,11 +1333,11 @@ int launch_cache_token(const CacheAttnParams& p, int tiles, int ctas, cudaStream
 template <int D>
 int launch_cache_join(const CacheAttnParams& p, const CachePlan& pl, int ctas, cudaStream_t st) {
   // the launch overlaps the end of the attention; the kernel waits for all of it
-  const int per_cta = 256 / (D / 4);
+  const int per_cta = kJoinThreads / (D / 4);
   const int rows = std::min(pl.item_tokens, p.s.num_tokens) * pl.group;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, std::min(8, (rows + per_cta - 1) / per_cta));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(ctas, std::min(32, (rows + per_cta - 1) / per_cta));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1351,7 +1355,7 @@ extern "C" size_t dynrad_cache_attn_workspace_bytes(const dynrad_kv_cache* cache
                                                     int32_t num_tokens, int32_t heads) {
   CachePlan pl;
   if (cache == nullptr || num_seqs < 0 || num_tokens < 0 || (cache->dim != 64 && cache->dim != 128) ||
-      cache_plan(cache, num_seqs, num_tokens, heads, &pl) != DYNRAD_OK)
+      cache_plan(cache, num_seqs, num_tokens, heads, INT64_MAX, &pl) != DYNRAD_OK)
     return 0;
   return pl.total;
 }
@@ -1366,13 +1370,16 @@ extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs
   if (rc != DYNRAD_OK) return rc;
   if (frame < 0 || window < 0 || (frame == 0 && window > 0)) return DYNRAD_ERR_INVALID_ARG;
   if (!(scale >= 0.0f) || !std::isfinite(scale)) return DYNRAD_ERR_INVALID_ARG;
-  if ((rc = cache_plan(cache, p.s.num_seqs, p.s.num_tokens, heads, &pl)) != DYNRAD_OK) return rc;
+  if ((rc = cache_plan(cache, p.s.num_seqs, p.s.num_tokens, heads,
+                       static_cast<int64_t>(seqs->max_pages) * cache->page, &pl)) != DYNRAD_OK)
+    return rc;
   if (p.s.num_seqs == 0 || p.s.num_tokens == 0) return DYNRAD_OK;
   if (bad_rows(q, q_token_stride, q_head_stride) || bad_rows(o, o_token_stride, o_head_stride) || lse == nullptr ||
       workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return DYNRAD_ERR_INVALID_ARG;
   if ((heads > 1 && q_head_stride == 0) || (p.s.num_tokens > 1 && q_token_stride == 0)) return DYNRAD_ERR_INVALID_ARG;
-  if (workspace_bytes < pl.total) return DYNRAD_ERR_CAPACITY;
+  if (workspace_bytes < dynrad_cache_attn_workspace_bytes(cache, p.s.num_seqs, p.s.num_tokens, heads))
+    return DYNRAD_ERR_CAPACITY;
   const float sc = scale == 0.0f ? 1.0f / std::sqrt(static_cast<float>(cache->dim)) : scale;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -1400,6 +1407,7 @@ extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return DYNRAD_ERR_CUDA;
   const int ctas = std::min(sms, kCacheMaxCtas) * pl.ctas_per_sm;
+  static_assert(CacheTokenCfg<128, 1>::kCtasPerSm * kCacheMaxCtas <= kJoinMost, "parts of an item");
   cudaStream_t st = as_stream(stream);
   if (pl.token_tiles > 0) {
     const bool e4m3 = cache->format == DYNRAD_CACHE_E4M3;
