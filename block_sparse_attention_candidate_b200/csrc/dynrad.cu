@@ -1115,6 +1115,7 @@ int check_cache(const dynrad_kv_cache* c, const dynrad_seqs* s, CacheDev* cd, Se
   if (c == nullptr || s == nullptr || c->k == nullptr || c->v == nullptr) return DYNRAD_ERR_INVALID_ARG;
   if (c->format < DYNRAD_CACHE_BF16 || c->format > DYNRAD_CACHE_INT8) return DYNRAD_ERR_INVALID_ARG;
   if (c->num_pages < 1 || c->heads < 1) return DYNRAD_ERR_INVALID_ARG;
+  if (c->heads > 65535) return DYNRAD_ERR_UNSUPPORTED;
   if (c->dim != 64 && c->dim != 128) return DYNRAD_ERR_UNSUPPORTED;
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return DYNRAD_ERR_UNSUPPORTED;
   if (c->num_pages > INT32_MAX || c->num_pages * c->heads > INT32_MAX / c->page) return DYNRAD_ERR_UNSUPPORTED;
@@ -1150,13 +1151,15 @@ bool bad_rows(const void* p, int64_t token_stride, int64_t head_stride) {
          (head_stride & 7) != 0;
 }
 
-int cache_move_grid(const SeqsDev& s, unsigned* grid) {
+// Tokens a CTA takes (one while the SMs have room for as many CTAs), and how many CTAs.
+int cache_move_grid(const SeqsDev& s, int32_t* tokens, unsigned* grid) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return DYNRAD_ERR_CUDA;
-  const int64_t chunks = (static_cast<int64_t>(s.num_tokens) + kCacheTokens - 1) / kCacheTokens;
-  *grid = static_cast<unsigned>(std::min<int64_t>(chunks, static_cast<int64_t>(sms) * 8));
+  const int64_t room = static_cast<int64_t>(sms) * kCacheCtasPerSm, n = s.num_tokens;
+  *tokens = static_cast<int32_t>(std::min<int64_t>(kCacheTokens, (n + room - 1) / room));
+  *grid = static_cast<unsigned>((n + *tokens - 1) / *tokens);
   return DYNRAD_OK;
 }
 
@@ -1179,20 +1182,20 @@ int cache_move_grid(const SeqsDev& s, unsigned* grid) {
 extern "C" int dynrad_cache_write(const dynrad_kv_cache* cache, const dynrad_seqs* seqs, const void* k,
                                   int64_t k_token_stride, int64_t k_head_stride, const void* v,
                                   int64_t v_token_stride, int64_t v_head_stride, dynrad_stream_t stream) {
-  CacheWriteParams p;
+  CacheMoveParams p = {};
   int rc = check_cache(cache, seqs, &p.c, &p.s);
   if (rc != DYNRAD_OK) return rc;
   if (p.s.num_seqs == 0 || p.s.num_tokens == 0) return DYNRAD_OK;
   if (bad_rows(k, k_token_stride, k_head_stride) || bad_rows(v, v_token_stride, v_head_stride))
     return DYNRAD_ERR_INVALID_ARG;
-  p.k = static_cast<const __nv_bfloat16*>(k);
-  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_in = static_cast<const __nv_bfloat16*>(k);
+  p.v_in = static_cast<const __nv_bfloat16*>(v);
   p.k_token = k_token_stride;
   p.k_head = k_head_stride;
   p.v_token = v_token_stride;
   p.v_head = v_head_stride;
   unsigned grid = 0;
-  if ((rc = cache_move_grid(p.s, &grid)) != DYNRAD_OK) return rc;
+  if ((rc = cache_move_grid(p.s, &p.tokens, &grid)) != DYNRAD_OK) return rc;
 #define DYNRAD_CACHE_F(D_, F_) cache_write_kernel<D_, F_><<<grid, kCacheThreads, 0, as_stream(stream)>>>(p)
   DYNRAD_CACHE_DISPATCH(cache->dim, cache->format, DYNRAD_CACHE_F);
 #undef DYNRAD_CACHE_F
@@ -1202,20 +1205,20 @@ extern "C" int dynrad_cache_write(const dynrad_kv_cache* cache, const dynrad_seq
 extern "C" int dynrad_cache_read(const dynrad_kv_cache* cache, const dynrad_seqs* seqs, void* k,
                                  int64_t k_token_stride, int64_t k_head_stride, void* v, int64_t v_token_stride,
                                  int64_t v_head_stride, dynrad_stream_t stream) {
-  CacheReadParams p;
+  CacheMoveParams p = {};
   int rc = check_cache(cache, seqs, &p.c, &p.s);
   if (rc != DYNRAD_OK) return rc;
   if (p.s.num_seqs == 0 || p.s.num_tokens == 0) return DYNRAD_OK;
   if (bad_rows(k, k_token_stride, k_head_stride) || bad_rows(v, v_token_stride, v_head_stride))
     return DYNRAD_ERR_INVALID_ARG;
-  p.k = static_cast<__nv_bfloat16*>(k);
-  p.v = static_cast<__nv_bfloat16*>(v);
+  p.k_out = static_cast<__nv_bfloat16*>(k);
+  p.v_out = static_cast<__nv_bfloat16*>(v);
   p.k_token = k_token_stride;
   p.k_head = k_head_stride;
   p.v_token = v_token_stride;
   p.v_head = v_head_stride;
   unsigned grid = 0;
-  if ((rc = cache_move_grid(p.s, &grid)) != DYNRAD_OK) return rc;
+  if ((rc = cache_move_grid(p.s, &p.tokens, &grid)) != DYNRAD_OK) return rc;
 #define DYNRAD_CACHE_F(D_, F_) cache_read_kernel<D_, F_><<<grid, kCacheThreads, 0, as_stream(stream)>>>(p)
   DYNRAD_CACHE_DISPATCH(cache->dim, cache->format, DYNRAD_CACHE_F);
 #undef DYNRAD_CACHE_F
@@ -1258,7 +1261,7 @@ int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, i
   pl->ctas_per_sm = pl->token_tiles == 0 ? 1 : (pl->token_tiles == 1 ? CacheTokenCfg<128, 1>::kCtasPerSm
                                                                       : CacheTokenCfg<128, 2>::kCtasPerSm);
   const int64_t slots = static_cast<int64_t>(num_tokens) / pl->item_tokens + num_seqs;
-  if (slots > INT32_MAX || c->heads > 65535) return DYNRAD_ERR_UNSUPPORTED;
+  if (slots > INT32_MAX) return DYNRAD_ERR_UNSUPPORTED;
   pl->slots = static_cast<int32_t>(slots);
   // The even cut pays while items are few or single sequences may be most of the
   // work.  Full items in many waves leave little to even out, and keep a head's

@@ -19,7 +19,8 @@
 //
 // Both kernels are one pass over the data and bound by HBM: per (token, head)
 // they move 2 * D * 2 bytes of bf16 and 2 * (D + D / 32) of the 8-bit pages
-// (2 * D * 2 again for bf16 pages).
+// (2 * D * 2 again for bf16 pages).  Small calls are bound by the chain of loads that
+// finds a token's place (sequence, its bounds, its page): 5-6 us a launch.
 #pragma once
 
 #include "common.cuh"
@@ -68,12 +69,16 @@ __device__ __forceinline__ SeqSpan seq_span(const SeqsDev& s, int i, int page_sh
   return r;
 }
 
-// The sequence that token t belongs to, -1 if none (t lies behind the last one).
+// The sequence that token t belongs to, -1 if none (t lies behind the last one).  A
+// warp's search, 32 entries at a time: one round trip for 32 sequences, two for 1024.
 __device__ __forceinline__ int seq_of_token(const SeqsDev& s, int t) {
+  const int lane = threadIdx.x & 31;
   int lo = 0, hi = s.num_seqs;   // last i with cu_seq[i] <= t
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s.cu_seq[mid] <= t) lo = mid; else hi = mid;
+    const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+    const int n = __popc(__ballot_sync(0xffffffffu, i < hi && s.cu_seq[i] <= t));
+    lo += max(n - 1, 0) * step;
+    hi = min(lo + step, hi);
   }
   return s.cu_seq[lo] <= t && t < s.cu_seq[lo + 1] ? lo : -1;
 }
@@ -211,108 +216,131 @@ __device__ __forceinline__ int scale_exponent(uint32_t a) {
 }
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheTokens = 8;   // tokens a CTA takes at a time
+// A CTA takes up to 8 tokens (one for each warp to look up) and goes through them head
+// by head, tokens inside: runs of 8 rows in the pages, which are head-major.  Measured
+// over 32,760 tokens of 40 heads (write e4m3 / write bf16 / read e4m3, us): heads
+// inside 216 / 252 / 212; tokens inside, 32 tokens 189 / 268 / 212, 16 tokens 183 /
+// 228 / 189, 8 tokens 183 / 216 / 171; with four units' loads in flight (here) 173 /
+// 220 / 169, which is 5.9-6.1 TB/s.
+constexpr int kCacheTokens = 8;
+constexpr int kCacheCtasPerSm = 4;
+constexpr int kCacheUnroll = 4;    // units whose loads a thread has in flight
 
-struct CacheWriteParams {
+struct CacheMoveParams {
   CacheDev c;
   SeqsDev s;
-  const __nv_bfloat16* k;
-  const __nv_bfloat16* v;
+  const __nv_bfloat16* k_in;       // writing: from the tokens' rows
+  const __nv_bfloat16* v_in;
+  __nv_bfloat16* k_out;            // reading back: to them
+  __nv_bfloat16* v_out;
   int64_t k_token, k_head, v_token, v_head;   // strides in elements
-};
-
-struct CacheReadParams {
-  CacheDev c;
-  SeqsDev s;
-  __nv_bfloat16* k;
-  __nv_bfloat16* v;
-  int64_t k_token, k_head, v_token, v_head;
+  int32_t tokens;                  // tokens a CTA takes
 };
 
 constexpr int64_t kRowNone = -1;     // nothing to do for this token
 constexpr int64_t kRowZero = -2;     // read back as zeros
 
-// Cache rows of kCacheTokens tokens from t0 on, by the CTA's first threads.
-__device__ __forceinline__ void place_tokens(const CacheDev& c, const SeqsDev& s, int t0, int64_t* rows) {
-  if (threadIdx.x < kCacheTokens) {
-    const int t = t0 + threadIdx.x;
+// Cache rows of the CTA's n tokens from t0 on, a warp a token.
+__device__ __forceinline__ void place_tokens(const CacheDev& c, const SeqsDev& s, int t0, int n, int64_t* rows) {
+  static_assert(kCacheTokens <= kCacheThreads / 32, "a warp a token");
+  const int i = threadIdx.x >> 5;
+  if (i < n) {
+    const int t = t0 + i, seq = seq_of_token(s, t);
     int64_t row = kRowNone;
-    if (t < s.num_tokens) {
-      const int seq = seq_of_token(s, t);
-      if (seq >= 0) {
-        const SeqSpan sp = seq_span(s, seq, c.page_shift);
-        const int32_t pos = sp.len - (sp.end - t);
-        row = pos < 0 || t >= sp.end ? kRowZero : cache_row(c, s, seq, pos);
-        if (row < 0) row = kRowZero;
-      }
+    if (seq >= 0) {
+      const SeqSpan sp = seq_span(s, seq, c.page_shift);
+      const int32_t pos = sp.len - (sp.end - t);
+      row = pos < 0 || t >= sp.end ? kRowZero : cache_row(c, s, seq, pos);
+      if (row < 0) row = kRowZero;
     }
-    rows[threadIdx.x] = row;
+    if ((threadIdx.x & 31) == 0) rows[i] = row;
   }
 }
 
-// One thread quantises (or copies) 16 channels of K or V of one (token, head):
-// two 16-byte loads, one 16-byte store (two for bf16), its neighbour shares the
-// scale.
+// Unit u of a CTA's n tokens: 16 channels (chunk c of C) of K (kv = 0) or V of one
+// (token, head), the tokens of a head together.
+struct CacheUnit {
+  int tk, kv, h, c;
+};
+
+template <int C>
+__device__ __forceinline__ CacheUnit cache_unit(uint32_t u, int heads, uint32_t n) {
+  CacheUnit x;
+  const uint32_t r = u / C, q = r / n;
+  x.c = u % C;
+  x.tk = r - q * n;
+  x.kv = q >= static_cast<uint32_t>(heads) ? 1 : 0;
+  x.h = static_cast<int>(q) - x.kv * heads;
+  return x;
+}
+
+// A thread quantises (or copies) a unit: two 16-byte loads, one 16-byte store (two
+// for bf16); its neighbour has the other half of the 32 channels under the scale.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheWriteParams p) {
-  constexpr int C = D / 16;   // threads a row
+__global__ void __launch_bounds__(kCacheThreads, kCacheCtasPerSm) cache_write_kernel(const CacheMoveParams p) {
+  constexpr int C = D / 16;
   __shared__ int64_t rows[kCacheTokens];
-  const int per_token = p.c.heads * 2 * C;
-  for (int t0 = blockIdx.x * kCacheTokens; t0 < p.s.num_tokens; t0 += gridDim.x * kCacheTokens) {
-    __syncthreads();
-    place_tokens(p.c, p.s, t0, rows);
-    __syncthreads();
-    const int units = min(kCacheTokens, p.s.num_tokens - t0) * per_token;
-    for (int u = threadIdx.x; u < ((units + 31) & ~31); u += kCacheThreads) {
-      const int tk = min(u, units - 1) / per_token;
-      const int r = min(u, units - 1) - tk * per_token;
-      const int c = r % C, kv = (r / C) / p.c.heads, h = (r / C) - kv * p.c.heads;
-      const int64_t row = u < units ? rows[tk] : kRowNone;
-      const bool live = row >= 0;
-      uint32_t x[8] = {};
-      if (live) {
-        const __nv_bfloat16* src = kv == 0 ? p.k + (t0 + tk) * p.k_token + h * p.k_head
-                                           : p.v + (t0 + tk) * p.v_token + h * p.v_head;
-        const uint4 a = *reinterpret_cast<const uint4*>(src + c * 16);
-        const uint4 b = *reinterpret_cast<const uint4*>(src + c * 16 + 8);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  const int heads = p.c.heads;
+  const int t0 = blockIdx.x * p.tokens;
+  const int n = min(p.tokens, p.s.num_tokens - t0), units = n * heads * 2 * C;   // even
+  place_tokens(p.c, p.s, t0, n, rows);
+  __syncthreads();
+  for (int u0 = threadIdx.x; u0 < ((units + 31) & ~31); u0 += kCacheThreads * kCacheUnroll) {
+    CacheUnit un[kCacheUnroll];
+    int64_t row[kCacheUnroll];
+    uint4 a[kCacheUnroll], b[kCacheUnroll];
+#pragma unroll
+    for (int i = 0; i < kCacheUnroll; ++i) {
+      const int u = u0 + i * kCacheThreads;
+      un[i] = cache_unit<C>(min(u, units - 1), heads, n);
+      row[i] = u < units ? rows[un[i].tk] : kRowNone;
+      a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row[i] >= 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            (un[i].kv == 0 ? p.k_in + (t0 + un[i].tk) * p.k_token + un[i].h * p.k_head
+                           : p.v_in + (t0 + un[i].tk) * p.v_token + un[i].h * p.v_head) + un[i].c * 16);
+        a[i] = __ldcs(src);
+        b[i] = __ldcs(src + 1);
       }
-      const int64_t at = row + (static_cast<int64_t>(h) << p.c.page_shift);
-      uint8_t* base = kv == 0 ? p.c.k : p.c.v;
+    }
+#pragma unroll
+    for (int i = 0; i < kCacheUnroll; ++i) {
+      const int64_t at = row[i] + (static_cast<int64_t>(un[i].h) << p.c.page_shift);
+      uint8_t* base = un[i].kv == 0 ? p.c.k : p.c.v;
       if (FMT == kCacheBf16) {
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(base + at * (D * 2) + c * 32);
-          dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-          dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        if (row[i] >= 0) {
+          uint4* dst = reinterpret_cast<uint4*>(base + at * (D * 2) + un[i].c * 32);
+          dst[0] = a[i];
+          dst[1] = b[i];
         }
       } else {
+        uint32_t x[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, x[i] & 0x7fff7fffu);
-        uint32_t a = max(m & 0xffffu, m >> 16);
-        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-        const bool nan = a >= 0x7f80u;
+        for (int j = 0; j < 8; ++j) m = __vmaxu2(m, x[j] & 0x7fff7fffu);
+        uint32_t most = max(m & 0xffffu, m >> 16);
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        const bool nan = most >= 0x7f80u;
         // magnitudes that would round to 2^128, past bf16, are held at the largest that does not
         constexpr uint32_t kMost = FMT == kCacheE4m3 ? 0x7f707f70u : 0x7f7e7f7eu;   // 240 * 2^120, 127 * 2^121
-        if (!nan && a > (kMost & 0xffffu)) {
-          a = kMost & 0xffffu;
+        if (!nan && most > (kMost & 0xffffu)) {
+          most = kMost & 0xffffu;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __vminu2(x[i] & 0x7fff7fffu, kMost) | (x[i] & 0x80008000u);
+          for (int j = 0; j < 8; ++j) x[j] = __vminu2(x[j] & 0x7fff7fffu, kMost) | (x[j] & 0x80008000u);
         }
-        const int e = nan ? 0 : scale_exponent<FMT>(a);
+        const int e = nan ? 0 : scale_exponent<FMT>(most);
         const uint32_t f = pow2_bf16x2(-e);
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t y0 = mul_bf16x2(x[2 * i], f), y1 = mul_bf16x2(x[2 * i + 1], f);
-          w[i] = nan ? 0u : pack4<FMT>(y0, y1);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t y0 = mul_bf16x2(x[2 * j], f), y1 = mul_bf16x2(x[2 * j + 1], f);
+          w[j] = nan ? 0u : pack4<FMT>(y0, y1);
         }
-        if (live) {
-          *reinterpret_cast<uint4*>(base + at * D + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-          if ((c & 1) == 0) {
-            uint8_t* sc = kv == 0 ? p.c.k_scale : p.c.v_scale;
-            sc[at * (D / kCacheGroup) + (c >> 1)] = nan ? kCacheNanScale : static_cast<uint8_t>(e + 127);
+        if (row[i] >= 0) {
+          *reinterpret_cast<uint4*>(base + at * D + un[i].c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          if ((un[i].c & 1) == 0) {
+            uint8_t* sc = un[i].kv == 0 ? p.c.k_scale : p.c.v_scale;
+            sc[at * (D / kCacheGroup) + (un[i].c >> 1)] = nan ? kCacheNanScale : static_cast<uint8_t>(e + 127);
           }
         }
       }
@@ -321,38 +349,54 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheReadParams p) {
+__global__ void __launch_bounds__(kCacheThreads, kCacheCtasPerSm) cache_read_kernel(const CacheMoveParams p) {
   constexpr int C = D / 16;
   __shared__ int64_t rows[kCacheTokens];
-  const int per_token = p.c.heads * 2 * C;
-  for (int t0 = blockIdx.x * kCacheTokens; t0 < p.s.num_tokens; t0 += gridDim.x * kCacheTokens) {
-    __syncthreads();
-    place_tokens(p.c, p.s, t0, rows);
-    __syncthreads();
-    const int units = min(kCacheTokens, p.s.num_tokens - t0) * per_token;
-    for (int u = threadIdx.x; u < units; u += kCacheThreads) {
-      const int tk = u / per_token, r = u - tk * per_token;
-      const int c = r % C, kv = (r / C) / p.c.heads, h = (r / C) - kv * p.c.heads;
-      const int64_t row = rows[tk];
-      if (row == kRowNone) continue;
-      uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-      if (row >= 0) {
-        const int64_t at = row + (static_cast<int64_t>(h) << p.c.page_shift);
-        const uint8_t* base = kv == 0 ? p.c.k : p.c.v;
+  const int heads = p.c.heads;
+  const int t0 = blockIdx.x * p.tokens;
+  const int n = min(p.tokens, p.s.num_tokens - t0), units = n * heads * 2 * C;
+  place_tokens(p.c, p.s, t0, n, rows);
+  __syncthreads();
+  for (int u0 = threadIdx.x; u0 < units; u0 += kCacheThreads * kCacheUnroll) {
+    CacheUnit un[kCacheUnroll];
+    int64_t row[kCacheUnroll];
+    uint4 a[kCacheUnroll], b[kCacheUnroll];
+    uint32_t byte[kCacheUnroll];
+#pragma unroll
+    for (int i = 0; i < kCacheUnroll; ++i) {
+      const int u = u0 + i * kCacheThreads;
+      un[i] = cache_unit<C>(min(u, units - 1), heads, n);
+      row[i] = u < units ? rows[un[i].tk] : kRowNone;
+      a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+      byte[i] = 127u;
+      if (row[i] >= 0) {
+        const int64_t at = row[i] + (static_cast<int64_t>(un[i].h) << p.c.page_shift);
+        const uint8_t* base = un[i].kv == 0 ? p.c.k : p.c.v;
         if (FMT == kCacheBf16) {
-          const uint4* src = reinterpret_cast<const uint4*>(base + at * (D * 2) + c * 32);
-          a = src[0];
-          b = src[1];
+          const uint4* src = reinterpret_cast<const uint4*>(base + at * (D * 2) + un[i].c * 32);
+          a[i] = __ldcs(src);
+          b[i] = __ldcs(src + 1);
         } else {
-          const uint8_t* sc = kv == 0 ? p.c.k_scale : p.c.v_scale;
-          const uint4 w = *reinterpret_cast<const uint4*>(base + at * D + c * 16);
-          dequant16<FMT>(w, sc[at * (D / kCacheGroup) + (c >> 1)], a, b);
+          const uint8_t* sc = un[i].kv == 0 ? p.c.k_scale : p.c.v_scale;
+          a[i] = __ldcs(reinterpret_cast<const uint4*>(base + at * D + un[i].c * 16));
+          byte[i] = sc[at * (D / kCacheGroup) + (un[i].c >> 1)];
         }
       }
-      __nv_bfloat16* dst = kv == 0 ? p.k + (t0 + tk) * p.k_token + h * p.k_head
-                                   : p.v + (t0 + tk) * p.v_token + h * p.v_head;
-      reinterpret_cast<uint4*>(dst + c * 16)[0] = a;
-      reinterpret_cast<uint4*>(dst + c * 16)[1] = b;
+    }
+#pragma unroll
+    for (int i = 0; i < kCacheUnroll; ++i) {
+      if (row[i] == kRowNone) continue;
+      if (FMT != kCacheBf16) {
+        uint4 o0, o1;
+        dequant16<FMT>(a[i], byte[i], o0, o1);
+        a[i] = row[i] >= 0 ? o0 : make_uint4(0u, 0u, 0u, 0u);
+        b[i] = row[i] >= 0 ? o1 : make_uint4(0u, 0u, 0u, 0u);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(
+          (un[i].kv == 0 ? p.k_out + (t0 + un[i].tk) * p.k_token + un[i].h * p.k_head
+                         : p.v_out + (t0 + un[i].tk) * p.v_token + un[i].h * p.v_head) + un[i].c * 16);
+      dst[0] = a[i];
+      dst[1] = b[i];
     }
   }
 }

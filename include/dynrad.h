@@ -490,7 +490,7 @@ typedef struct dynrad_kv_cache {
   uint8_t *k_scale; /* DEVICE, 16-byte aligned; ignored for bf16 */
   uint8_t *v_scale;
   int64_t num_pages; /* num_pages * heads * page < 2^31 */
-  int32_t heads;     /* K / V heads */
+  int32_t heads;     /* K / V heads, at most 65535 */
   int32_t page;      /* tokens a page: 16, 32, 64 or 128 */
   int32_t dim;       /* 64 or 128 */
   int32_t format;    /* dynrad_cache_format */
