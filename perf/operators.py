@@ -277,9 +277,8 @@ def run(st):
             abi.dynrad_cache_write(cache, st["new_k"], st["new_v"], st["table"], st["cu"], st["length"])
             return st["k"], st["v"], st["ks"], st["vs"]
         if c["op"] == "read":
-            k, v = abi.dynrad_cache_read(cache, st["table"], st["cu"], st["length"], st["tokens"],
+            return abi.dynrad_cache_read(cache, st["table"], st["cu"], st["length"], st["tokens"],
                                          head_major=c["head_major"])
-            return (k.transpose(0, 1), v.transpose(0, 1)) if c["head_major"] else (k, v)
         return abi.dynrad_cache_attn(st["q"], cache, st["table"], st["cu"], st["length"], frame=c["frame"],
                                      window=c["window"])
     return {"write": _write, "read": _read, "attend": _attend}[c["op"]](st)
