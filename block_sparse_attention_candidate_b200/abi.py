@@ -653,13 +653,16 @@ def dynrad_cache_write(cache, k, v, page_table, cu_seq, kv_len, stream=None) -> 
     """Writes K and V (bf16 [T, heads, D], any strides that are multiples of 8)
     into the cache: token i of the n that cu_seq gives sequence s goes to its
     position kv_len[s] - n + i (kv_len counts the new tokens)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dynrad_cache_write(cache, k, v, page_table, cu_seq, kv_len)
     T = k.shape[0]
     sq = _cache_seqs(cache, page_table, cu_seq, kv_len, T)
     kt, kh = _cache_rows(cache, "k", k, cache.heads)
     vt, vh = _cache_rows(cache, "v", v, cache.heads, T)
     _require_current(cache)
     _check(lib().dynrad_cache_write(ctypes.byref(cache.c), ctypes.byref(sq), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                                    _stream(stream)), "dynrad_cache_write")
+                                    _stream()), "dynrad_cache_write")
 
 
 def dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens=None, head_major=False, out=None, stream=None):
@@ -668,6 +671,9 @@ def dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens=None, head_m
     dynrad_select_blocks and dynrad_sparse_attn take, but for the batch axis).
     T = num_tokens, or that of the tensors in ``out``; rows behind
     cu_seq[-1] are left as they are."""
+    if stream is not None:    # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens, head_major, out)
     if out is None:
         if num_tokens is None:
             raise ValueError("num_tokens or out is needed")
@@ -682,7 +688,7 @@ def dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens=None, head_m
     vt, vh = _cache_rows(cache, "out", v, cache.heads, T, head_major, written=True)
     _require_current(cache)
     _check(lib().dynrad_cache_read(ctypes.byref(cache.c), ctypes.byref(sq), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                                   _stream(stream)), "dynrad_cache_read")
+                                   _stream()), "dynrad_cache_read")
     return k, v
 
 
@@ -694,6 +700,9 @@ def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, s
     that many positions (1: token-causal); window >= 1: of those the last
     ``window`` frames.  Returns (o bf16 [T, heads, D], lse fp32 [heads, T]); rows
     behind cu_seq[-1] are left as they are."""
+    if stream is not None:    # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame, window, scale, out, lse, workspace)
     if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache.heads:
         raise ValueError("q must be [T, heads, D] with a multiple of the cache's heads")
     T, H, D = q.shape
@@ -715,5 +724,5 @@ def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, s
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _check(L.dynrad_cache_attn(ctypes.byref(cache.c), ctypes.byref(sq), q.data_ptr(), qt, qh, H, int(frame),
                                int(window), float(scale), o.data_ptr(), ot, oh, lse_t.data_ptr(),
-                               workspace.data_ptr(), workspace.numel(), _stream(stream)), "dynrad_cache_attn")
+                               workspace.data_ptr(), workspace.numel(), _stream()), "dynrad_cache_attn")
     return o, lse_t

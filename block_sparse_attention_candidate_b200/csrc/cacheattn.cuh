@@ -727,7 +727,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
         head = run->head;
         place = run->place;
       }
-      if (lane < 2) p.part_desc[2 * blockIdx.x + lane] = make_int4(0, 0, kPartNone, 0);
+      if (lane == 0)
+        p.part_desc[2 * blockIdx.x] = p.part_desc[2 * blockIdx.x + 1] = make_int4(0, 0, kPartNone, 0);
     } else {
       head = blockIdx.y;
       place = p.slots - 1 - static_cast<int>(blockIdx.x);   // later tokens see more: longest first

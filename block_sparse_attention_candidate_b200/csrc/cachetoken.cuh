@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
     off = left > 0 ? run->off : 0;
     head = left > 0 ? run->head : 0;
     place = left > 0 ? run->place : 0;
-    if (threadIdx.x < 2) p.part_desc[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, kPartNone, 0);
+    if (threadIdx.x == 0)
+      p.part_desc[2 * blockIdx.x] = p.part_desc[2 * blockIdx.x + 1] = make_int4(0, 0, kPartNone, 0);
   } else {
     head = blockIdx.y;
     place = p.slots - 1 - static_cast<int>(blockIdx.x);

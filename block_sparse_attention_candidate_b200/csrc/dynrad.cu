@@ -5,6 +5,7 @@
 // below.
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdio>
@@ -1126,7 +1127,8 @@ int check_cache(const dynrad_kv_cache* c, const dynrad_seqs* s, CacheDev* cd, Se
   if (s->num_seqs < 0 || s->num_tokens < 0 || s->max_pages < 0 || s->table_stride < s->max_pages)
     return DYNRAD_ERR_INVALID_ARG;
   if (s->max_pages > (INT32_MAX - 255) / c->page) return DYNRAD_ERR_UNSUPPORTED;
-  if (s->num_seqs > 0 && (s->page_table == nullptr || s->cu_seq == nullptr || s->kv_len == nullptr))
+  if (s->num_seqs > 0 &&
+      ((s->page_table == nullptr && s->max_pages > 0) || s->cu_seq == nullptr || s->kv_len == nullptr))
     return DYNRAD_ERR_INVALID_ARG;
   cd->k = static_cast<uint8_t*>(c->k);
   cd->v = static_cast<uint8_t*>(c->v);
@@ -1372,7 +1374,8 @@ extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs
   int rc = check_cache(cache, seqs, &p.c, &p.s);
   if (rc != DYNRAD_OK) return rc;
   if (frame < 0 || window < 0 || (frame == 0 && window > 0)) return DYNRAD_ERR_INVALID_ARG;
-  if (!(scale >= 0.0f) || !std::isfinite(scale)) return DYNRAD_ERR_INVALID_ARG;
+  // the kernels multiply a masked logit's -inf by the scale, flushing subnormals
+  if (!(scale == 0.0f || scale >= FLT_MIN) || !std::isfinite(scale * 1.4426950408889634f)) return DYNRAD_ERR_INVALID_ARG;
   if ((rc = cache_plan(cache, p.s.num_seqs, p.s.num_tokens, heads,
                        static_cast<int64_t>(seqs->max_pages) * cache->page, &pl)) != DYNRAD_OK)
     return rc;

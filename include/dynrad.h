@@ -567,7 +567,7 @@ int dynrad_cache_read(const dynrad_kv_cache *cache, const dynrad_seqs *seqs,
  *   q, o          DEVICE bf16, 16-byte aligned; strides in elements, multiples of
  *                 8, as in dynrad_cache_write; o must not overlap q
  *   heads         query heads, a multiple of cache->heads, at most 128 to each
- *   scale         logit scale; 0 means 1/sqrt(dim)
+ *   scale         logit scale, a normal number; 0 means 1/sqrt(dim)
  *   lse           DEVICE fp32 [heads, num_tokens]
  *   workspace     DEVICE, 256-byte aligned, at least
  *                 dynrad_cache_attn_workspace_bytes(...) bytes (0 if it can not

@@ -23,11 +23,13 @@ class Batch:
     Table entries behind a sequence's last page lead nowhere; `spare` columns
     and rows' padding are part of the table's stride."""
 
-    def __init__(self, ns, lens, page, seed=0, tail=0, pad_cols=1, lead_pages=0):
+    def __init__(self, ns, lens, page, seed=0, tail=0, pad_cols=1, lead_pages=0, keys=0, skip=0):
+        """keys: what the table's rows can hold at least (the library cuts items into
+        parts only where that is over 1024); skip: rows before the first sequence's."""
         rng = np.random.default_rng(seed)
         self.ns, self.lens, self.page = list(ns), list(lens), page
         used = [-(-n // page) for n in lens]
-        self.cols = max(used + [1])
+        self.cols = max(used + [1, -(-keys // page)])
         self.num_pages = lead_pages + sum(used) + 2
         order = lead_pages + rng.permutation(self.num_pages - lead_pages)
         wide = np.array([[NOWHERE[(s + c) % 4] for c in range(self.cols + pad_cols)] for s in range(len(ns))],
@@ -37,7 +39,7 @@ class Batch:
             wide[s, :u] = order[at:at + u]
             at += u
         self.table_np = wide[:, :self.cols]
-        self.cu_np = np.concatenate([[0], np.cumsum(ns)]).astype(np.int64)
+        self.cu_np = skip + np.concatenate([[0], np.cumsum(ns)]).astype(np.int64)
         self.tokens = int(self.cu_np[-1]) + tail
         self.tail = tail
         self.table = torch.from_numpy(wide.astype(np.int32)).cuda()[:, :self.cols]

@@ -30,7 +30,7 @@ BAD_STRUCTS = [
     (dict(k=None), {}, 1), (dict(v=None), {}, 1), (dict(k=P + 8), {}, 1), (dict(k_scale=None), {}, 1),
     (dict(v_scale=P + 4), {}, 1), (dict(format=3), {}, 1), (dict(format=-1), {}, 1), (dict(num_pages=0), {}, 1),
     (dict(heads=0), {}, 1), (dict(dim=96), {}, 2), (dict(dim=256), {}, 2), (dict(page=48), {}, 2),
-    (dict(page=8), {}, 2), (dict(page=256), {}, 2), (dict(num_pages=1 << 25), {}, 2),
+    (dict(page=8), {}, 2), (dict(page=256), {}, 2), (dict(heads=1 << 16), {}, 2), (dict(num_pages=1 << 25), {}, 2),
     ({}, dict(cu_seq=None), 1), ({}, dict(page_table=None), 1), ({}, dict(kv_len=None), 1),
     ({}, dict(num_seqs=-1), 1), ({}, dict(num_tokens=-1), 1), ({}, dict(max_pages=-1), 1),
     ({}, dict(table_stride=3), 1), ({}, dict(max_pages=1 << 26, table_stride=1 << 26), 2),
@@ -68,7 +68,8 @@ def test_bad_operands_refused_before_launch():
     assert attn(heads=258) == 2                                  # 129 query heads to a K / V head
     assert attn(frame=-1) == 1 and attn(window=-1) == 1 and attn(frame=0, window=2) == 1
     assert attn(scale=-1.0) == 1 and attn(scale=math.nan) == 1 and attn(scale=math.inf) == 1
-    assert attn(qt=500) == 1 and attn(oh=4) == 1
+    assert attn(scale=1e-40) == 1 and attn(scale=3e38) == 1
+    assert attn(qt=500) == 1 and attn(oh=4) == 1 and attn(qt=0) == 1 and attn(qh=0) == 1
     assert attn(ws_bytes=16) == abi.DYNRAD_ERR_CAPACITY
     assert L.dynrad_cache_attn_workspace_bytes(c, 3, 7, 3) == 0
     assert L.dynrad_cache_attn_workspace_bytes(c, -1, 7, 4) == 0

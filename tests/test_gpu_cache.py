@@ -137,9 +137,10 @@ BATCHES = {
 @pytest.mark.parametrize("name", list(BATCHES))
 @pytest.mark.parametrize("heads,kv_heads,page,frame,window", [
     (2, 2, 16, 1, 0), (6, 2, 32, 1, 40), (5, 1, 64, 0, 0), (8, 1, 128, 24, 3)])
-def test_attention_matches_the_oracle(fmt, dim, name, heads, kv_heads, page, frame, window):
+@pytest.mark.parametrize("cut", [False, True])
+def test_attention_matches_the_oracle(fmt, dim, name, heads, kv_heads, page, frame, window, cut):
     ns, lens = BATCHES[name]
-    b = Batch(ns, lens, page, seed=len(name), tail=3)
+    b = Batch(ns, lens, page, seed=len(name), tail=3, keys=1100 if cut else 0, skip=2)
     g = gen(dim + len(name))
     c, kk, kv = filled_cache(b, kv_heads, dim, fmt, g)
     q = torch.randn((b.tokens, heads, dim), generator=g, device="cuda").bfloat16()
@@ -149,7 +150,8 @@ def test_attention_matches_the_oracle(fmt, dim, name, heads, kv_heads, page, fra
     torch.cuda.synchronize()
     check_device_status()
     check_attention(o, lse, q, kk, kv, b, frame, window)
-    assert (o[b.cu_np[-1]:] == 7.0).all() and (lse[:, b.cu_np[-1]:] == 7.0).all()
+    for nobodys in (slice(0, 2), slice(int(b.cu_np[-1]), None)):
+        assert (o[nobodys] == 7.0).all() and (lse[:, nobodys] == 7.0).all()
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -178,10 +180,11 @@ def test_items_cut_into_parts(fmt, ns, lens, heads, kv_heads, dim, page, frame, 
     ([900, 1, 830, 0, 60], [950, 70, 830, 5, 300], 192, 12),
     ([1] * 2100, [1 + i % 37 for i in range(2100)], 2, 1),      # more places than a CTA scans
 ])
-def test_calls_of_many_items(ns, lens, heads, kv_heads):
-    b = Batch(ns, lens, 32, seed=1)
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_calls_of_many_items(ns, lens, heads, kv_heads, fmt):
+    b = Batch(ns, lens, 32, seed=1, keys=1100)
     g = gen(len(ns))
-    c, kk, kv = filled_cache(b, kv_heads, 64, "int8", g)
+    c, kk, kv = filled_cache(b, kv_heads, 64, fmt, g)
     q = torch.randn((b.tokens, heads, 64), generator=g, device="cuda").bfloat16()
     o, lse = abi.dynrad_cache_attn(q, c, *b.call())
     torch.cuda.synchronize()
@@ -224,6 +227,19 @@ def test_head_groups_and_layouts(heads, kv_heads):
     check_device_status()
 
 
+@pytest.mark.parametrize("frame,window", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1), (7, 1), (130, 1)])
+def test_extreme_frames_and_windows(frame, window):
+    for fmt, ns in (("bf16", [40, 1]), ("fp8", [40, 1]), ("fp8", [1, 2])):
+        b = Batch(ns, [290, 131], 16, seed=6, keys=1100)
+        g = gen(8)
+        c, kk, kv = filled_cache(b, 1, 64, fmt, g)
+        q = torch.randn((b.tokens, 3, 64), generator=g, device="cuda").bfloat16()
+        o, lse = abi.dynrad_cache_attn(q, c, *b.call(), frame=frame, window=window)
+        torch.cuda.synchronize()
+        check_device_status()
+        check_attention(o, lse, q, kk, kv, b, frame, window)
+
+
 @pytest.mark.parametrize("scale", [0.02, 0.7])
 def test_logit_scale_and_strong_logits(scale):
     b = Batch([1, 70], [260, 200], 64, seed=6)
@@ -238,10 +254,11 @@ def test_logit_scale_and_strong_logits(scale):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("frame,window", [(1, 0), (1, 20), (16, 2)])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
-def test_what_a_row_does_not_see_cannot_reach_it(fmt, frame, window, bad):
+@pytest.mark.parametrize("ns,cut", [([100, 1], False), ([100, 1], True), ([2, 3], True)])
+def test_what_a_row_does_not_see_cannot_reach_it(fmt, frame, window, bad, ns, cut):
     """A token whose K and V hold NaN or infinity, inside the cache: rows that do
     not see it are those of the finite cache, rows that see it are not finite."""
-    b = Batch([100, 1], [150, 140], 32, seed=8)
+    b = Batch(ns, [112, 33] if ns == [2, 3] else [150, 140], 32, seed=8, keys=1100 if cut else 0)
     g = gen(3)
     w = b.whole()
     k, v = (torch.randn((w.tokens, 2, 64), generator=g, device="cuda").bfloat16() for _ in range(2))
@@ -398,7 +415,7 @@ def test_a_video_written_and_attended_frame_by_frame(fmt):
 
 
 def test_calls_on_other_streams_and_captured():
-    b = Batch([1, 90, 3], [700, 300, 64], 32, seed=7)
+    b = Batch([1, 90, 3], [2700, 300, 64], 32, seed=7)
     g = gen(2)
     c, kk, kv = filled_cache(b, 2, 128, "fp8", g)
     q = torch.randn((b.tokens, 8, 128), generator=g, device="cuda").bfloat16()
@@ -411,9 +428,20 @@ def test_calls_on_other_streams_and_captured():
     torch.cuda.synchronize()
     for o, lse in ((o1, lse1), (o2, lse2)):
         assert torch.equal(o, o_ref) and torch.equal(lse, lse_ref)
+    # the stream as an argument: what the call allocates is that stream's
+    side.wait_stream(torch.cuda.current_stream())
+    o3, lse3 = abi.dynrad_cache_attn(q, c, *b.call(), stream=side)
+    k3, v3 = abi.dynrad_cache_read(c, *b.call(), b.tokens, stream=side)
+    c3 = empty_cache(b, 2, 128, "fp8")
+    side.wait_stream(torch.cuda.current_stream())
+    abi.dynrad_cache_write(c3, k3, v3, *b.call(), stream=side)
+    side.synchronize()
+    assert torch.equal(o3, o_ref) and torch.equal(lse3, lse_ref)
+    k4, _ = abi.dynrad_cache_read(c3, *b.call(), b.tokens)
+    assert torch.equal(k4, k3)
     # a decode step captured once: write, attend; replayed with new inputs and lengths
-    ns, lens = [1, 1, 1], [100, 40, 700]
-    b = Batch(ns, [n + 3 for n in lens], 32, seed=11)
+    ns, lens = [1, 1, 1], [100, 40, 2700]
+    b = Batch(ns, [n + 3 for n in lens], 32, seed=11, keys=1100)
     w = b.whole()
     k, v = (torch.randn((w.tokens, 2, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
     c = empty_cache(b, 2, 128, "int8")
