@@ -1,12 +1,14 @@
-// Attention of single tokens (16 rows at most of a sequence and K / V head) over
-// 8-bit pages: the same mathematics and schedule as cacheattn.cuh, for calls whose
-// time is the reading of the cache.
+// Attention of single tokens (16 rows at most of a sequence and K / V head): the same
+// mathematics and schedule as cacheattn.cuh, for calls whose time is the reading of the
+// cache, or a call's latency.
 //
-// The tensor-core tiles of cacheattn.cuh want bf16 operands in shared memory.  For
-// few rows that detour is the bound: 64 KB written and 96 KB read again by the
-// products for every 33 KB of 128 keys.  Here a warp turns the stored bytes into
-// register fragments of 16 x 8 x 16 products (warp_mma.cuh) and nothing goes back:
-// shared memory holds the bytes alone, once written and once read.
+// The tensor-core tiles of cacheattn.cuh are 128 rows high whatever the rows, and want
+// bf16 operands in shared memory.  For 8-bit pages and few rows that detour is the
+// bound: 64 KB written and 96 KB read again by the products for every 33 KB of 128
+// keys; and one row's softmax over 128 keys takes one thread some 2,900 clocks.  Here
+// a warp turns the stored bytes into register fragments of 16 x 8 x 16 products
+// (warp_mma.cuh) and nothing goes back: shared memory holds the bytes alone, once
+// written and once read, and 128 keys are eight warps' work.
 //
 // The keys are the products' 16 rows, since there are more of them than query rows:
 // S^T = K Q^T and O^T = V^T P^T, with 8 query rows a column tile (NT = 1 or 2 of
@@ -28,10 +30,10 @@
 // row r takes place 2 (r & 3) + r / 4 of its eight and V's chunk c is at
 // c ^ ((r / 2) & 3).
 //
-// A CTA has eight warps and an SM three CTAs (NT = 1) or two; a segment's 16-key
-// blocks go to the warps in turn, each warp with a ring of its own, filled by
-// cp.async, and its own max, sum and O.  At the end of a segment the eight are joined
-// in shared memory while the SM's other CTAs read on.
+// A CTA has eight warps (bf16: six) and an SM three CTAs (NT = 1, 8-bit) or two; a
+// segment's 16-key blocks go to the warps in turn, each warp with a ring of its own,
+// filled by cp.async, and its own max, sum and O.  At the end of a segment they are
+// joined in shared memory while the SM's other CTAs read on.
 #pragma once
 
 #include "cacheattn.cuh"
@@ -39,25 +41,33 @@
 
 namespace dynrad {
 
-constexpr int kTokenWarps = 8;
-constexpr int kTokenThreads = kTokenWarps * 32;
 constexpr int kTokenKeys = 16;       // keys of a block
 
-template <int D, int NT>
+template <int D, int FMT, int NT>
 struct CacheTokenCfg {
+  static constexpr bool kRaw = FMT != kCacheBf16;
   static constexpr int kRows = 8 * NT;                          // rows of an item
-  static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
-  static constexpr int kCodes = kTokenKeys * D;
-  static constexpr int kScales = kTokenKeys * (D / kCacheGroup);
+  static constexpr int kWarps = kRaw ? 8 : 6;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCtasPerSm = kRaw && NT == 1 ? 3 : 2;
+  static constexpr int kRowBytes = kRaw ? D : 2 * D;            // a key's K or V as stored
+  static constexpr int kCodes = kTokenKeys * kRowBytes;
+  static constexpr int kScales = kRaw ? kTokenKeys * (D / kCacheGroup) : 0;
   static constexpr int kStageBytes = 2 * (kCodes + kScales);    // K, V, K's scales, V's scales
-  static constexpr int kStages = (NT == 1 ? 2 : 3) * (128 / D);
+  static constexpr int kStages = (kRaw && NT == 2 ? 3 : 2) * (128 / D);
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kQ = NT * (D / 16) * 256;                // Q's operands, 8 bytes a step and lane
-  static constexpr int kCtrl = 256 + kTokenWarps * kRows * 8;
-  static constexpr int kSmem = kTokenWarps * kRingBytes + kQ + kCtrl;
+  static constexpr int kCtrl = 256 + kWarps * kRows * 8;
+  static constexpr int kSmem = kWarps * kRingBytes + kQ + kCtrl;
   static_assert(kRows * D * 4 <= kRingBytes, "a warp's O over its ring");
   static_assert(kCtasPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
+
+// CTAs of a split launch on an SM
+constexpr int token_ctas_per_sm(bool raw, int nt) {
+  return raw ? (nt == 1 ? CacheTokenCfg<128, kCacheInt8, 1>::kCtasPerSm : CacheTokenCfg<128, kCacheInt8, 2>::kCtasPerSm)
+             : (nt == 1 ? CacheTokenCfg<128, kCacheBf16, 1>::kCtasPerSm : CacheTokenCfg<128, kCacheBf16, 2>::kCtasPerSm);
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
@@ -95,55 +105,14 @@ struct TokenState {
   uint32_t flip;              // unpack_pair's constant
 };
 
-// One block of 16 keys from key0 on, its bytes at st.  partial: some row of the item,
-// which sees [lo, hi) and every row of it [lo_max, hi_min), does not see all of it.  odd: some scale's factor takes more
-// than a shift of its byte (odd_scale); such blocks are rare.
-template <int D, int FMT, int NT>
-__device__ __forceinline__ void token_block(TokenState<D, NT>& me, const uint8_t* st, int key0, bool partial, bool odd,
-                                            int32_t lo, int32_t hi, int32_t lo_max, int32_t hi_min, float scale_log2,
-                                            const uint32_t (&kbyte)[2][D / 64],
-                                            uint32_t (&vbyte)[4], const uint2* qs, volatile int* poison) {
-  constexpr int KW = D / 64, VB = D / 8, NJ = D / 16;
-  using C = CacheTokenCfg<D, NT>;
-  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-  // S^T = K Q^T
-  float s[NT][4] = {};
-#pragma unroll
-  for (int w = 0; w < KW; ++w) {
-    uint32_t kf[2][2][4];     // [key row][operand register][step]
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const uint4 x = *reinterpret_cast<const uint4*>(st + n * 8 * D + (w == 0 ? me.k_off : me.k_off ^ 64));
-      const uint32_t f = odd ? kBf16One : kbyte[n][w] * 0x00800080u + kUnpackBias<FMT> * 0x00800080u;
-      unpack4<FMT>(x.x, kf[n][0][0], kf[n][1][0]);
-      unpack4<FMT>(x.y, kf[n][0][1], kf[n][1][1]);
-      unpack4<FMT>(x.z, kf[n][0][2], kf[n][1][2]);
-      unpack4<FMT>(x.w, kf[n][0][3], kf[n][1][3]);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) kf[n][e][u] = mul_bf16x2(kf[n][e][u], f);
-    }
-    if (odd) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        uint32_t f1, f2;
-        scale_factors<FMT>(kbyte[n][w], f1, f2);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) kf[n][e][u] = mul_bf16x2(mul_bf16x2(kf[n][e][u], f1), f2);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint2 q = qs[(n * NJ + w * 4 + u) * 32];
-        mma_16816(s[n], kf[0][0][u], kf[1][0][u], kf[0][1][u], kf[1][1][u], q.x, q.y);
-      }
-  }
-  // s[n][2 i + e]: key 8 i + 4 (g & 1) + g / 2, query row 8 n + 2 t + e
+// From S^T of a block to P^T as the second product's operand, in bf16; updates max, sum
+// and, when a max grew by more than 2^8, O.
+// s[n][2 i + e]: key 8 i + 4 (g & 1) + g / 2, query row 8 n + 2 t + e
+template <int D, int NT>
+__device__ __forceinline__ void token_softmax(TokenState<D, NT>& me, float (&s)[NT][4], int key0, bool partial,
+                                              float scale_log2, uint32_t (&pf)[NT][2]) {
+  constexpr int NJ = D / 16;
+  const int g = (threadIdx.x & 31) >> 2;
   if (partial) {
     const int key = key0 + 4 * (g & 1) + (g >> 1);
 #pragma unroll
@@ -152,7 +121,6 @@ __device__ __forceinline__ void token_block(TokenState<D, NT>& me, const uint8_t
       for (int u = 0; u < 4; ++u)
         if (key + 8 * (u >> 1) < me.rlo[n][u & 1] || key + 8 * (u >> 1) >= me.rhi[n][u & 1]) s[n][u] = -INFINITY;
   }
-  uint32_t pf[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float mx[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])}, m_new[2];
@@ -188,6 +156,58 @@ __device__ __forceinline__ void token_block(TokenState<D, NT>& me, const uint8_t
     pf[n][0] = transpose8x8(pack_bf16x2(p[0], p[1]));
     pf[n][1] = transpose8x8(pack_bf16x2(p[2], p[3]));
   }
+}
+
+// One block of 16 keys from key0 on, its bytes at st.  partial: some row of the item,
+// which sees [lo, hi) and every row of it [lo_max, hi_min), does not see all of it.  odd: some scale's factor takes more
+// than a shift of its byte (odd_scale); such blocks are rare.
+template <int D, int FMT, int NT>
+__device__ __forceinline__ void token_block(TokenState<D, NT>& me, const uint8_t* st, int key0, bool partial, bool odd,
+                                            int32_t lo, int32_t hi, int32_t lo_max, int32_t hi_min, float scale_log2,
+                                            const uint32_t (&kbyte)[2][D / 64],
+                                            uint32_t (&vbyte)[4], const uint2* qs, volatile int* poison) {
+  constexpr int KW = D / 64, VB = D / 8, NJ = D / 16;
+  using C = CacheTokenCfg<D, FMT, NT>;
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  // S^T = K Q^T
+  float s[NT][4] = {};
+  uint32_t pf[NT][2];
+#pragma unroll
+  for (int w = 0; w < KW; ++w) {
+    uint32_t kf[2][2][4];     // [key row][operand register][step]
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const uint4 x = *reinterpret_cast<const uint4*>(st + n * 8 * D + (w == 0 ? me.k_off : me.k_off ^ 64));
+      const uint32_t f = odd ? kBf16One : kbyte[n][w] * 0x00800080u + kUnpackBias<FMT> * 0x00800080u;
+      unpack4<FMT>(x.x, kf[n][0][0], kf[n][1][0]);
+      unpack4<FMT>(x.y, kf[n][0][1], kf[n][1][1]);
+      unpack4<FMT>(x.z, kf[n][0][2], kf[n][1][2]);
+      unpack4<FMT>(x.w, kf[n][0][3], kf[n][1][3]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) kf[n][e][u] = mul_bf16x2(kf[n][e][u], f);
+    }
+    if (odd) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        uint32_t f1, f2;
+        scale_factors<FMT>(kbyte[n][w], f1, f2);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) kf[n][e][u] = mul_bf16x2(mul_bf16x2(kf[n][e][u], f1), f2);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint2 q = qs[(n * NJ + w * 4 + u) * 32];
+        mma_16816(s[n], kf[0][0][u], kf[1][0][u], kf[0][1][u], kf[1][1][u], q.x, q.y);
+      }
+  }
+  token_softmax<D, NT>(me, s, key0, partial, scale_log2, pf);
   // O^T += V^T P^T: V rows t, 4 + t (first keys of the sum), 8 + t, 12 + t
   uint32_t x[4][VB / 4];
 #pragma unroll
@@ -253,16 +273,69 @@ __device__ __forceinline__ void token_block(TokenState<D, NT>& me, const uint8_t
   }
 }
 
+// The same for bf16 pages: ldmatrix brings both operands as the products want them, K's
+// and V's rows named as above (row i of eight is key 4 (i & 1) + i / 2), channels in
+// order.  Chunk c of a row lies at c ^ (row & 7).
+template <int D, int NT>
+__device__ __forceinline__ void token_block_bf16(TokenState<D, NT>& me, const uint8_t* st, int key0, bool partial,
+                                                 int32_t lo, int32_t hi, int32_t lo_max, int32_t hi_min,
+                                                 float scale_log2, const uint2* qs, volatile int* poison) {
+  constexpr int NJ = D / 16, RB = 2 * D;
+  const int lane = threadIdx.x & 31, i = lane & 7;
+  const int key = 4 * (i & 1) + (i >> 1);
+  const uint32_t base = smem_u32(st);
+  // lane's row of the four 8 x 8 matrices: K: keys, keys + 8, then the next eight
+  // channels; V: keys, the next channels, then keys + 8
+  const int krow = key + ((lane >> 3) & 1) * 8, kc = lane >> 4;
+  const int vrow = key + (lane >> 4) * 8, vc = (lane >> 3) & 1;
+  float s[NT][4] = {};
+  uint32_t pf[NT][2];
+#pragma unroll
+  for (int u = 0; u < NJ; ++u) {
+    uint32_t a0, a1, a2, a3;
+    ldsm_x4(base + krow * RB + (((2 * u + kc) ^ key) << 4), a0, a1, a2, a3);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint2 q = qs[(n * NJ + u) * 32];
+      mma_16816(s[n], a0, a1, a2, a3, q.x, q.y);
+    }
+  }
+  token_softmax<D, NT>(me, s, key0, partial, scale_log2, pf);
+  if (partial) {     // what no row sees, and what is not finite of what some see, stay out (cacheattn.cuh)
+#pragma unroll 1
+    for (int u = lane; u < kTokenKeys * (D / 8); u += 32) {
+      const int r = u / (D / 8), k = key0 + r;
+      if (k >= lo_max && k < hi_min) continue;
+      uint4* at = reinterpret_cast<uint4*>(const_cast<uint8_t*>(st) + kTokenKeys * RB) + u;
+      const uint4 x = *at;
+      uint4 y = make_uint4(0u, 0u, 0u, 0u);
+      if (k >= lo && k < hi) {
+        y = make_uint4(finite_bf16x2(x.x), finite_bf16x2(x.y), finite_bf16x2(x.z), finite_bf16x2(x.w));
+        if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *poison = 1;
+      }
+      *at = y;
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    uint32_t a0, a1, a2, a3;
+    ldsm_x4_trans(base + kTokenKeys * RB + vrow * RB + (((2 * j + vc) ^ key) << 4), a0, a1, a2, a3);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mma_16816(me.o[n][j], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+  }
+}
+
 template <int D, int FMT, int NT>
-__global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerSm)
+__global__ void __launch_bounds__(CacheTokenCfg<D, FMT, NT>::kThreads, CacheTokenCfg<D, FMT, NT>::kCtasPerSm)
     cache_token_kernel(const CacheAttnParams p) {
-  using C = CacheTokenCfg<D, NT>;
+  using C = CacheTokenCfg<D, FMT, NT>;
   constexpr int KW = D / 64;                 // 16-byte chunks of a key that a thread reads
   constexpr int VB = D / 8;                  // bytes of a V row that a thread reads: 16 or 8
   constexpr int NJ = D / 16;                 // channel tiles, and steps of K Q^T
   extern __shared__ __align__(128) uint8_t token_smem[];
-  uint2* q_s = reinterpret_cast<uint2*>(token_smem + kTokenWarps * C::kRingBytes);   // [row tile][step][lane]
-  uint8_t* ctrl = token_smem + kTokenWarps * C::kRingBytes + C::kQ;
+  uint2* q_s = reinterpret_cast<uint2*>(token_smem + C::kWarps * C::kRingBytes);   // [row tile][step][lane]
+  uint8_t* ctrl = token_smem + C::kWarps * C::kRingBytes + C::kQ;
   CacheRun* run = reinterpret_cast<CacheRun*>(ctrl);
   volatile int* poison = reinterpret_cast<volatile int*>(ctrl + 32);
   CacheSeg* seg_s = reinterpret_cast<CacheSeg*>(ctrl + 64);
@@ -276,7 +349,7 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
   int place, head;
   int64_t off = 0, left = 1;
   if (p.split) {
-    plan_run<kTokenThreads>(p, item_tokens, reinterpret_cast<int32_t*>(token_smem), reinterpret_cast<int64_t*>(ml), run);
+    plan_run<C::kThreads>(p, item_tokens, reinterpret_cast<int32_t*>(token_smem), reinterpret_cast<int64_t*>(ml), run);
     left = run->left;
     off = left > 0 ? run->off : 0;
     head = left > 0 ? run->head : 0;
@@ -303,11 +376,11 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
   me.v_off1 = v_place(t + 4);
   me.flip = 0x00800080u ^ (gridDim.z - 1u);   // gridDim.z is 1: a constant that stays in a register
   // scale bytes: of this thread's key and chunk, and of V row t and its channels
-  const int ks_off = 2 * C::kCodes + krow * (D / kCacheGroup) + (t >> 1);
-  const int vs_off = 2 * C::kCodes + C::kScales + t * (D / kCacheGroup) + vc * VB / kCacheGroup;
+  [[maybe_unused]] const int ks_off = 2 * C::kCodes + krow * (D / kCacheGroup) + (t >> 1);
+  [[maybe_unused]] const int vs_off = 2 * C::kCodes + C::kScales + t * (D / kCacheGroup) + vc * VB / kCacheGroup;
   // where this lane's 16-byte chunks of a block go: chunk u = lane + 32 i is row
   // u / (D / 16); i = 2, 3 (D = 128) lie eight rows further on
-  int k_dst[2], v_dst[2];
+  [[maybe_unused]] int k_dst[2], v_dst[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int u = lane + 32 * i, r = u / (D / 16), c = u % (D / 16);
@@ -366,7 +439,7 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
     left = seg_s->narrow ? max(left, static_cast<int64_t>(1)) : 0;   // warp 0 keeps the count
 
     const int rows = it.ntok * p.group;
-    // 16-key blocks [b0, b1) of the segment; this warp has b0 + warp, + 8, ..
+    // 16-key blocks [b0, b1) of the segment; this warp has every kWarps-th
     const int64_t ka = max(static_cast<int64_t>(it.lo), static_cast<int64_t>(it.step0 + sa) << 7);
     const int64_t kb = min(static_cast<int64_t>(it.hi), static_cast<int64_t>(it.step0 + sb) << 7);
     const int b0 = static_cast<int>(ka >> 4), b1 = sb > sa ? static_cast<int>((kb + 15) >> 4) : b0;
@@ -378,18 +451,27 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
         if (!good && lane == 0) record_error(DYNRAD_ERR_DEVICE);
         // a page outside the pool is filled with zeros
         const int64_t row = good ? (((static_cast<int64_t>(pg) * p.c.heads + kvh) << ps) + ((b << 4) & ((1 << ps) - 1))) : 0;
-        const uint8_t* kc = p.c.k + row * D + lane * 16;
-        const uint8_t* vcodes = p.c.v + row * D + lane * 16;
+        const uint8_t* kc = p.c.k + row * C::kRowBytes + lane * 16;
+        const uint8_t* vcodes = p.c.v + row * C::kRowBytes + lane * 16;
         const uint32_t dst = ring_u + stage * C::kStageBytes;
+        if constexpr (C::kRaw) {
 #pragma unroll
-        for (int i = 0; i < C::kCodes / 512; ++i) {
-          cp_async16(dst + k_dst[i & 1] + (i >> 1) * 1024, kc + i * 512, good);
-          cp_async16(dst + v_dst[i & 1] + (i >> 1) * 1024, vcodes + i * 512, good);
-        }
-        constexpr int W = C::kScales / 4;     // 16 or 8 words each
-        if (lane < 2 * W) {
-          const uint8_t* sc = (lane < W ? p.c.k_scale : p.c.v_scale) + row * (D / kCacheGroup) + (lane % W) * 4;
-          cp_async4(dst + 2 * C::kCodes + lane * 4, sc, good);
+          for (int i = 0; i < C::kCodes / 512; ++i) {
+            cp_async16(dst + k_dst[i & 1] + (i >> 1) * 1024, kc + i * 512, good);
+            cp_async16(dst + v_dst[i & 1] + (i >> 1) * 1024, vcodes + i * 512, good);
+          }
+          constexpr int W = C::kScales / 4;     // 16 or 8 words each
+          if (lane < 2 * W) {
+            const uint8_t* sc = (lane < W ? p.c.k_scale : p.c.v_scale) + row * (D / kCacheGroup) + (lane % W) * 4;
+            cp_async4(dst + 2 * C::kCodes + lane * 4, sc, good);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < C::kCodes / 512; ++i) {
+            const int u = lane + 32 * i, r = u / (D / 8), to = r * C::kRowBytes + (((u % (D / 8)) ^ (r & 7)) << 4);
+            cp_async16(dst + to, kc + i * 512, good);
+            cp_async16(dst + C::kCodes + to, vcodes + i * 512, good);
+          }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -398,25 +480,27 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
     {
       int32_t pg[C::kStages];
 #pragma unroll
-      for (int s = 0; s < C::kStages; ++s) pg[s] = page_of(b + s * kTokenWarps);
+      for (int s = 0; s < C::kStages; ++s) pg[s] = page_of(b + s * C::kWarps);
 #pragma unroll
-      for (int s = 0; s < C::kStages; ++s) load(b + s * kTokenWarps, pg[s], s);
+      for (int s = 0; s < C::kStages; ++s) load(b + s * C::kWarps, pg[s], s);
     }
-    int32_t next_page = page_of(b + C::kStages * kTokenWarps);
+    int32_t next_page = page_of(b + C::kStages * C::kWarps);
 
-    // Q's operands: query row 8 n + g, step u: of chunk t + 4 (u / 4) the channels of
-    // word u % 4; a warp brings a step
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = 8 * n + g, tok = r / p.group;
-      if (warp < NJ) {
-        uint2 q = make_uint2(0u, 0u);
-        if (r < rows)
-          q = *reinterpret_cast<const uint2*>(p.q + (it.tok0 + tok) * p.q_token +
-                                              (kvh * p.group + r - tok * p.group) * p.q_head +
-                                              (t + 4 * (warp >> 2)) * 16 + (warp & 3) * 4);
-        q_s[(n * NJ + warp) * 32 + lane] = q;
+    // Q's operands: query row 8 n + g, step u.  8-bit: of chunk t + 4 (u / 4) the channels
+    // of word u % 4; bf16: channels 16 u + 2 t and 16 u + 8 + 2 t
+    for (int x = warp; x < NT * NJ; x += C::kWarps) {
+      const int u = x % NJ, r = 8 * (x / NJ) + g, tok = r / p.group;
+      uint2 q = make_uint2(0u, 0u);
+      if (r < rows) {
+        const __nv_bfloat16* src = p.q + (it.tok0 + tok) * p.q_token + (kvh * p.group + r - tok * p.group) * p.q_head;
+        if constexpr (C::kRaw) {
+          q = *reinterpret_cast<const uint2*>(src + (t + 4 * (u >> 2)) * 16 + (u & 3) * 4);
+        } else {
+          q.x = *reinterpret_cast<const uint32_t*>(src + 16 * u + 2 * t);
+          q.y = *reinterpret_cast<const uint32_t*>(src + 16 * u + 8 + 2 * t);
+        }
       }
+      q_s[x * 32 + lane] = q;
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -435,31 +519,36 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
 
     int stage = 0;
 #pragma unroll 1
-    for (; b < b1; b += kTokenWarps) {
+    for (; b < b1; b += C::kWarps) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
       __syncwarp();
       const uint8_t* st = ring + stage * C::kStageBytes;
       const int key0 = b << 4;
       const bool partial = key0 < it.lo_max || key0 > it.hi_min - 16;
-      uint32_t kbyte[2][KW], vbyte[4];
-      bool odd = false;
+      if constexpr (C::kRaw) {
+        uint32_t kbyte[2][KW], vbyte[4];
+        bool odd = false;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          kbyte[n][w] = st[ks_off + n * 8 * (D / kCacheGroup) + w * 2];
-          odd = odd || odd_scale<FMT>(kbyte[n][w]);
+          for (int w = 0; w < KW; ++w) {
+            kbyte[n][w] = st[ks_off + n * 8 * (D / kCacheGroup) + w * 2];
+            odd = odd || odd_scale<FMT>(kbyte[n][w]);
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vbyte[i] = st[vs_off + i * 4 * (D / kCacheGroup)];
+          odd = odd || odd_scale<FMT>(vbyte[i]);
         }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        vbyte[i] = st[vs_off + i * 4 * (D / kCacheGroup)];
-        odd = odd || odd_scale<FMT>(vbyte[i]);
+        token_block<D, FMT, NT>(me, st, key0, partial, __any_sync(0xffffffffu, odd), it.lo, it.hi, it.lo_max,
+                                it.hi_min, p.scale_log2, kbyte, vbyte, q_s + lane, poison);
+      } else {
+        token_block_bf16<D, NT>(me, st, key0, partial, it.lo, it.hi, it.lo_max, it.hi_min, p.scale_log2, q_s + lane,
+                                poison);
       }
-      token_block<D, FMT, NT>(me, st, key0, partial, __any_sync(0xffffffffu, odd), it.lo, it.hi, it.lo_max,
-                              it.hi_min, p.scale_log2, kbyte, vbyte, q_s + lane, poison);
       __syncwarp();      // every lane has read the stage
-      load(b + C::kStages * kTokenWarps, next_page, stage);
-      next_page = page_of(b + (C::kStages + 1) * kTokenWarps);
+      load(b + C::kStages * C::kWarps, next_page, stage);
+      next_page = page_of(b + (C::kStages + 1) * C::kWarps);
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -474,22 +563,30 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
         for (int x = 4; x < 32; x <<= 1) me.l[n][e] += __shfl_xor_sync(0xffffffffu, me.l[n][e], x);
         const int r = 8 * n + 2 * t + e;
         if (g == 0) ml[warp * C::kRows + r] = make_float2(me.m[n][e], me.l[n][e]);
-        float* dst = reinterpret_cast<float*>(ring) + r * D + vc * VB;   // the thread's run of channels
+        float* dst = reinterpret_cast<float*>(ring) + r * D;
+        if constexpr (C::kRaw) {      // the thread's run of channels
 #pragma unroll
-        for (int j = 0; j < NJ; j += 2)
-          *reinterpret_cast<float4*>(dst + 2 * j) =
-              make_float4(me.o[n][j][e], me.o[n][j][2 + e], me.o[n][j + 1][e], me.o[n][j + 1][2 + e]);
+          for (int j = 0; j < NJ; j += 2)
+            *reinterpret_cast<float4*>(dst + vc * VB + 2 * j) =
+                make_float4(me.o[n][j][e], me.o[n][j][2 + e], me.o[n][j + 1][e], me.o[n][j + 1][2 + e]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            dst[16 * j + g] = me.o[n][j][e];
+            dst[16 * j + 8 + g] = me.o[n][j][2 + e];
+          }
+        }
       }
     __syncthreads();
     const bool poisoned = *poison != 0;
-    for (int u = threadIdx.x; u < rows * (D / 4); u += kTokenThreads) {
+    for (int u = threadIdx.x; u < rows * (D / 4); u += C::kThreads) {
       const int r = u / (D / 4), c = u % (D / 4);
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-      for (int w = 0; w < kTokenWarps; ++w) mm = fmaxf(mm, ml[w * C::kRows + r].x);
+      for (int w = 0; w < C::kWarps; ++w) mm = fmaxf(mm, ml[w * C::kRows + r].x);
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kTokenWarps; ++w) {
+      for (int w = 0; w < C::kWarps; ++w) {
         const float2 x = ml[w * C::kRows + r];
         const float f = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2_approx(x.x - mm);
         if (f == 0.f) continue;
@@ -508,9 +605,21 @@ __global__ void __launch_bounds__(kTokenThreads, CacheTokenCfg<D, NT>::kCtasPerS
         for (int key = first; key < last; ++key) {
           if (key >= it.lo_max && key < it.hi_min) continue;
           const int64_t at = cache_row(p.c, p.s, it.seq, key);
-          if (at >= 0 && p.c.v_scale[(at + (static_cast<int64_t>(kvh) << ps)) * (D / kCacheGroup) + c * 4 / kCacheGroup] ==
-                             kCacheNanScale)
-            a.x = a.y = a.z = a.w = __int_as_float(0x7fffffff);
+          if (at < 0) continue;
+          const int64_t row = at + (static_cast<int64_t>(kvh) << ps);
+          if constexpr (C::kRaw) {
+            if (p.c.v_scale[row * (D / kCacheGroup) + c * 4 / kCacheGroup] == kCacheNanScale)
+              a.x = a.y = a.z = a.w = __int_as_float(0x7fffffff);
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p.c.v + row * C::kRowBytes + c * 8);
+            auto add = [](float& to, uint32_t bits) {
+              if ((bits & 0x7f800000u) == 0x7f800000u) to += __uint_as_float(bits);
+            };
+            add(a.x, v.x << 16);
+            add(a.y, v.x & 0xffff0000u);
+            add(a.z, v.y << 16);
+            add(a.w, v.y & 0xffff0000u);
+          }
         }
       }
       const int64_t token = it.tok0 + tok;

@@ -1248,11 +1248,10 @@ int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, i
   pl->group = heads / c->heads;
   if (pl->group > 128) return DYNRAD_ERR_UNSUPPORTED;
   pl->tile_tokens = 128 / pl->group;
-  // 8-bit pages and sequences of 8 or 16 rows on average at most: the kernel that
-  // reads them once (TOKEN_FIGURES)
+  // sequences of 8 or 16 rows on average at most: the kernel of single tokens (TOKEN_FIGURES)
   pl->token_tiles = 0;
   for (int nt = 2; nt >= 1; --nt)
-    if (c->format != DYNRAD_CACHE_BF16 && pl->group <= 8 * nt &&
+    if (pl->group <= 8 * nt &&
         static_cast<int64_t>(num_tokens) <= static_cast<int64_t>(num_seqs) * (8 * nt / pl->group))
       pl->token_tiles = nt;
   if (pl->token_tiles > 0) pl->tile_tokens = 8 * pl->token_tiles / pl->group;
@@ -1260,8 +1259,7 @@ int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, i
   pl->tiles = static_cast<int64_t>(num_tokens) <= static_cast<int64_t>(num_seqs) * pl->tile_tokens ? 1 : 2;
   pl->item_tokens = pl->tiles * pl->tile_tokens;
   pl->part_rows = pl->token_tiles > 0 ? 8 * pl->token_tiles : 128 * pl->tiles;
-  pl->ctas_per_sm = pl->token_tiles == 0 ? 1 : (pl->token_tiles == 1 ? CacheTokenCfg<128, 1>::kCtasPerSm
-                                                                      : CacheTokenCfg<128, 2>::kCtasPerSm);
+  pl->ctas_per_sm = pl->token_tiles == 0 ? 1 : token_ctas_per_sm(c->format != DYNRAD_CACHE_BF16, pl->token_tiles);
   const int64_t slots = static_cast<int64_t>(num_tokens) / pl->item_tokens + num_seqs;
   if (slots > INT32_MAX) return DYNRAD_ERR_UNSUPPORTED;
   pl->slots = static_cast<int32_t>(slots);
@@ -1321,12 +1319,12 @@ int launch_cache_attn(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
 
 template <int D, int FMT, int NT>
 int launch_cache_token(const CacheAttnParams& p, int ctas, cudaStream_t st) {
-  using C = CacheTokenCfg<D, NT>;
+  using C = CacheTokenCfg<D, FMT, NT>;
   static OptInTable optin;   // per instantiation, per device
   const int rc = smem_optin(optin, reinterpret_cast<const void*>(cache_token_kernel<D, FMT, NT>), C::kSmem);
   if (rc != DYNRAD_OK) return rc;
   const dim3 grid = p.split ? dim3(ctas) : dim3(p.slots, p.c.heads);
-  cache_token_kernel<D, FMT, NT><<<grid, kTokenThreads, C::kSmem, st>>>(p);
+  cache_token_kernel<D, FMT, NT><<<grid, C::kThreads, C::kSmem, st>>>(p);
   return launch_status();
 }
 
@@ -1413,17 +1411,12 @@ extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return DYNRAD_ERR_CUDA;
   const int ctas = std::min(sms, kCacheMaxCtas) * pl.ctas_per_sm;
-  static_assert(CacheTokenCfg<128, 1>::kCtasPerSm * kCacheMaxCtas <= kJoinMost, "parts of an item");
+  static_assert(token_ctas_per_sm(true, 1) * kCacheMaxCtas <= kJoinMost, "parts of an item");
   cudaStream_t st = as_stream(stream);
   if (pl.token_tiles > 0) {
-    const bool e4m3 = cache->format == DYNRAD_CACHE_E4M3;
-    const int nt = pl.token_tiles;
-    if (cache->dim == 128)
-      rc = e4m3 ? launch_cache_token<128, kCacheE4m3>(p, nt, ctas, st)
-                : launch_cache_token<128, kCacheInt8>(p, nt, ctas, st);
-    else
-      rc = e4m3 ? launch_cache_token<64, kCacheE4m3>(p, nt, ctas, st)
-                : launch_cache_token<64, kCacheInt8>(p, nt, ctas, st);
+#define DYNRAD_CACHE_F(D_, F_) rc = launch_cache_token<D_, F_>(p, pl.token_tiles, ctas, st)
+    DYNRAD_CACHE_DISPATCH(cache->dim, cache->format, DYNRAD_CACHE_F);
+#undef DYNRAD_CACHE_F
   } else {
     CUtensorMap mq = {}, mk = {}, mv = {};
     const int64_t any = cache->dim;   // stride of an axis of length one: any that the map takes
