@@ -644,9 +644,12 @@ def _cache_rows(cache, name, t, heads, tokens=None, head_major=False, written=Fa
     return ts, hs
 
 
-def _require_current(cache):
-    if cache.device_index < 0 or cache.device_index != torch.cuda.current_device():
+def _cache_stream(cache):
+    """The current stream of the cache's device, which must be the current one."""
+    index = torch.cuda.current_device() if cache.device_index >= 0 else None
+    if cache.device_index != index:
         raise ValueError("the cache must be on the current CUDA device")
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def dynrad_cache_write(cache, k, v, page_table, cu_seq, kv_len, stream=None) -> None:
@@ -660,9 +663,9 @@ def dynrad_cache_write(cache, k, v, page_table, cu_seq, kv_len, stream=None) -> 
     sq = _cache_seqs(cache, page_table, cu_seq, kv_len, T)
     kt, kh = _cache_rows(cache, "k", k, cache.heads)
     vt, vh = _cache_rows(cache, "v", v, cache.heads, T)
-    _require_current(cache)
+    st = _cache_stream(cache)
     _check(lib().dynrad_cache_write(ctypes.byref(cache.c), ctypes.byref(sq), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                                    _stream()), "dynrad_cache_write")
+                                    st), "dynrad_cache_write")
 
 
 def dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens=None, head_major=False, out=None, stream=None):
@@ -678,7 +681,8 @@ def dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens=None, head_m
         if num_tokens is None:
             raise ValueError("num_tokens or out is needed")
         shape = (cache.heads, num_tokens) if head_major else (num_tokens, cache.heads)
-        out = tuple(torch.empty(shape + (cache.dim,), dtype=torch.bfloat16, device=cache.device) for _ in range(2))
+        shape += (cache.dim,)
+        out = cache.k.new_empty(shape, dtype=torch.bfloat16), cache.k.new_empty(shape, dtype=torch.bfloat16)
     k, v = out
     T = k.shape[1 if head_major else 0]
     if num_tokens is not None and num_tokens != T:
@@ -686,9 +690,9 @@ def dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens=None, head_m
     sq = _cache_seqs(cache, page_table, cu_seq, kv_len, T)
     kt, kh = _cache_rows(cache, "out", k, cache.heads, T, head_major, written=True)
     vt, vh = _cache_rows(cache, "out", v, cache.heads, T, head_major, written=True)
-    _require_current(cache)
+    st = _cache_stream(cache)
     _check(lib().dynrad_cache_read(ctypes.byref(cache.c), ctypes.byref(sq), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                                   _stream()), "dynrad_cache_read")
+                                   st), "dynrad_cache_read")
     return k, v
 
 
@@ -698,7 +702,7 @@ def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, s
     cache's) over what the cache holds, their own keys among it.  frame = 0: a
     token sees its whole sequence; frame >= 1: up to the end of its own frame of
     that many positions (1: token-causal); window >= 1: of those the last
-    ``window`` frames.  Returns (o bf16 [T, heads, D], lse fp32 [heads, T]); rows
+    ``window`` frames.  Returns (o bf16 [T, heads, D], laid out as q, and lse fp32 [heads, T]); rows
     behind cu_seq[-1] are left as they are."""
     if stream is not None:    # what is allocated here belongs to that stream too
         with torch.cuda.stream(stream):
@@ -710,19 +714,21 @@ def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, s
     qt, qh = _cache_rows(cache, "q", q, H)
     if (T > 1 and qt == 0) or (H > 1 and qh == 0):
         raise ValueError("q must not be expanded")
-    o = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+    o = torch.empty_like(q) if out is None else out      # in q's order of strides
     ot, oh = _cache_rows(cache, "out", o, H, T, written=True)
-    lse_t = torch.empty((H, T), dtype=torch.float32, device=q.device) if lse is None else lse
-    if lse_t.dtype != torch.float32 or lse_t.shape != (H, T) or not lse_t.is_contiguous() or lse_t.device != q.device:
+    if lse is None:
+        lse = q.new_empty((H, T), dtype=torch.float32)
+    elif (lse.dtype != torch.float32 or lse.shape != (H, T) or not lse.is_contiguous() or
+          lse.get_device() != cache.device_index):
         raise ValueError("lse must be a contiguous fp32 [heads, T] tensor")
-    _require_current(cache)
+    st = _cache_stream(cache)
     L = lib()
     if workspace is None:
         need = L.dynrad_cache_attn_workspace_bytes(ctypes.byref(cache.c), sq.num_seqs, T, H)
         if need == 0:
             raise DynradError(DYNRAD_ERR_INVALID_ARG, "dynrad_cache_attn_workspace_bytes")
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     _check(L.dynrad_cache_attn(ctypes.byref(cache.c), ctypes.byref(sq), q.data_ptr(), qt, qh, H, int(frame),
-                               int(window), float(scale), o.data_ptr(), ot, oh, lse_t.data_ptr(),
-                               workspace.data_ptr(), workspace.numel(), _stream()), "dynrad_cache_attn")
-    return o, lse_t
+                               int(window), float(scale), o.data_ptr(), ot, oh, lse.data_ptr(),
+                               workspace.data_ptr(), workspace.numel(), st), "dynrad_cache_attn")
+    return o, lse
