@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "tma2d.cuh"
 
 namespace dynrad {
 

@@ -53,6 +53,7 @@
 
 #include "attention.cuh"
 #include "kvcache.cuh"
+#include "tma2d.cuh"
 
 namespace dynrad {
 
