@@ -1077,12 +1077,22 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
   const int x = blockIdx.x;
   const int4 d0 = p.part_desc[2 * x + 1];
   if (d0.z != kPartOpen) return;
+  // the first later part that is not open ends the item; 32 descriptors at a look (one
+  // after the other: 3 us more at 19 parts)
+  const int lane = threadIdx.x & 31;
   int parts = 1;
-  while (x + parts < ctas) {
-    const int z = p.part_desc[2 * (x + parts)].z;
-    if (z == kPartNone) return;   // a launch that gave up (recorded): nothing to join
-    ++parts;
-    if (z == kPartLast) break;
+  while (true) {
+    const int at = x + parts + lane;
+    const int z = at < ctas ? p.part_desc[2 * at].z : kPartNone;
+    const uint32_t stop = __ballot_sync(0xffffffffu, z != kPartOpen);
+    if (stop == 0u) {
+      parts += 32;
+      continue;
+    }
+    const int first = __ffs(stop) - 1;
+    if (__shfl_sync(0xffffffffu, z, first) == kPartNone) return;   // a launch that gave up (recorded)
+    parts += first + 1;
+    break;
   }
   const CacheItem it = find_item(p, item_tokens, d0.x);
   // row = tile * 128 + token of the tile * group + head of the group

@@ -30,10 +30,19 @@
 // row r takes place 2 (r & 3) + r / 4 of its eight and V's chunk c is at
 // c ^ ((r / 2) & 3).
 //
-// A CTA has eight warps (bf16: six) and an SM three CTAs (NT = 1, 8-bit) or two; a
-// segment's 16-key blocks go to the warps in turn, each warp with a ring of its own,
-// filled by cp.async, and its own max, sum and O.  At the end of a segment they are
-// joined in shared memory while the SM's other CTAs read on.
+// A segment's 16-key blocks (8-bit: pairs of them) go to the warps in turn, each warp
+// with a ring of its own, filled by cp.async, and its own max, sum and O.  At the end of
+// a segment they are joined in shared memory while the SM's other CTAs read on.  An SM
+// runs twelve warps: two CTAs of six, or three of four (8-bit, NT = 1).
+//
+// Measured on 8 K / V heads of D 128 (times of the launch and its join):
+//   3 x 131072 keys, 64 heads: e4m3 168 us (4.9 TB/s), int8 154 (5.4), bf16 252 (6.4);
+//   64 sequences of up to 16000 keys, 32 heads: int8 189 us (5.2), bf16 295 (6.4).
+// 8-bit pages are bound by issue (unpacking a byte and scaling it), not by HBM.  Pairs
+// of blocks share the softmax step's shuffles and votes: with single blocks and eight
+// warps in each of three CTAs (80 registers) the 8-bit times were 182, 170 and 212 us;
+// with twelve warps in one CTA 160 and 213 (joined less often, but nothing reads on
+// meanwhile); in fours, 195 and 226 (one group in flight).
 #pragma once
 
 #include "cacheattn.cuh"
@@ -41,24 +50,28 @@
 
 namespace dynrad {
 
-constexpr int kTokenKeys = 16;       // keys of a block
+constexpr int kTokenKeys = 16;       // keys of a block, the unit of loads and products
 
 template <int D, int FMT, int NT>
 struct CacheTokenCfg {
   static constexpr bool kRaw = FMT != kCacheBf16;
   static constexpr int kRows = 8 * NT;                          // rows of an item
-  static constexpr int kWarps = kRaw ? 8 : 6;
+  static constexpr int kWarps = kRaw && NT == 1 ? 4 : 6;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtasPerSm = kRaw && NT == 1 ? 3 : 2;
+  // blocks a warp takes at a time: two neighbours of 8-bit pages share one softmax step,
+  // whose fixed costs weigh as much as a block's unpacking
+  static constexpr int kSub = kRaw ? 2 : 1;
   static constexpr int kRowBytes = kRaw ? D : 2 * D;            // a key's K or V as stored
   static constexpr int kCodes = kTokenKeys * kRowBytes;
   static constexpr int kScales = kRaw ? kTokenKeys * (D / kCacheGroup) : 0;
   static constexpr int kStageBytes = 2 * (kCodes + kScales);    // K, V, K's scales, V's scales
-  static constexpr int kStages = (kRaw && NT == 2 ? 3 : 2) * (128 / D);
+  static constexpr int kStages = (kRaw ? 4 : 2) * (128 / D);
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kQ = NT * (D / 16) * 256;                // Q's operands, 8 bytes a step and lane
   static constexpr int kCtrl = 256 + kWarps * kRows * 8;
   static constexpr int kSmem = kWarps * kRingBytes + kQ + kCtrl;
+  static_assert(kStages % kSub == 0, "whole groups of blocks");
   static_assert(kRows * D * 4 <= kRingBytes, "a warp's O over its ring");
   static_assert(kCtasPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
@@ -101,29 +114,39 @@ struct TokenState {
   float o[NT][D / 16][4];     // O^T: of channel tile j rows g, g + 8; query rows 2 t, 2 t + 1
   float m[NT][2], l[NT][2];   // of query rows 2 t, 2 t + 1: max (log2 units), this thread's part of the sum
   int32_t rlo[NT][2], rhi[NT][2];   // what those rows see
-  int k_off, v_off0, v_off1;  // where the thread reads (see the kernel)
+  int k_off, v_off0, v_off1, ks_off, vs_off;  // where the thread reads (see the kernel)
   uint32_t flip;              // unpack_pair's constant
 };
 
-// From S^T of a block to P^T as the second product's operand, in bf16; updates max, sum
-// and, when a max grew by more than 2^8, O.
-// s[n][2 i + e]: key 8 i + 4 (g & 1) + g / 2, query row 8 n + 2 t + e
-template <int D, int NT>
-__device__ __forceinline__ void token_softmax(TokenState<D, NT>& me, float (&s)[NT][4], int key0, bool partial,
-                                              float scale_log2, uint32_t (&pf)[NT][2]) {
+// From S^T of NB neighbouring blocks to P^T as the second products' operands, in bf16;
+// updates max, sum and, when a max grew by more than 2^8, O.
+// s[b][n][2 i + e]: key 16 b + 8 i + 4 (g & 1) + g / 2, query row 8 n + 2 t + e
+template <int D, int NT, int NB>
+__device__ __forceinline__ void token_softmax(TokenState<D, NT>& me, float (&s)[NB][NT][4], int key0, bool partial,
+                                              float scale_log2, uint32_t (&pf)[NB][NT][2]) {
   constexpr int NJ = D / 16;
   const int g = (threadIdx.x & 31) >> 2;
   if (partial) {
     const int key = key0 + 4 * (g & 1) + (g >> 1);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (key + 8 * (u >> 1) < me.rlo[n][u & 1] || key + 8 * (u >> 1) >= me.rhi[n][u & 1]) s[n][u] = -INFINITY;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int k = key + 16 * b + 8 * (u >> 1);
+          if (k < me.rlo[n][u & 1] || k >= me.rhi[n][u & 1]) s[b][n][u] = -INFINITY;
+        }
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float mx[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])}, m_new[2];
+    float mx[2], m_new[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      mx[e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
+#pragma unroll
+      for (int b = 1; b < NB; ++b) mx[e] = fmax3(mx[e], s[b][n][e], s[b][n][2 + e]);
+    }
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
@@ -145,135 +168,164 @@ __device__ __forceinline__ void token_softmax(TokenState<D, NT>& me, float (&s)[
         }
       }
     }
-    float p[4];
+    const float ref[2] = {me.m[n][0] == -INFINITY ? 0.f : me.m[n][0], me.m[n][1] == -INFINITY ? 0.f : me.m[n][1]};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float ref = me.m[n][e] == -INFINITY ? 0.f : me.m[n][e];
+    for (int b = 0; b < NB; ++b) {
+      float p[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) p[2 * i + e] = ex2_approx(fmaf(s[n][2 * i + e], scale_log2, -ref));
-      me.l[n][e] += p[e] + p[2 + e];
+      for (int u = 0; u < 4; ++u) p[u] = ex2_approx(fmaf(s[b][n][u], scale_log2, -ref[u & 1]));
+      me.l[n][0] += p[0] + p[2];
+      me.l[n][1] += p[1] + p[3];
+      pf[b][n][0] = transpose8x8(pack_bf16x2(p[0], p[1]));
+      pf[b][n][1] = transpose8x8(pack_bf16x2(p[2], p[3]));
     }
-    pf[n][0] = transpose8x8(pack_bf16x2(p[0], p[1]));
-    pf[n][1] = transpose8x8(pack_bf16x2(p[2], p[3]));
   }
 }
 
-// One block of 16 keys from key0 on, its bytes at st.  partial: some row of the item,
-// which sees [lo, hi) and every row of it [lo_max, hi_min), does not see all of it.  odd: some scale's factor takes more
-// than a shift of its byte (odd_scale); such blocks are rare.
+// Two blocks, 32 keys from key0 on, their bytes at st one after the other.  partial:
+// some row of the item, which sees [lo, hi) and every row of it [lo_max, hi_min), does
+// not see all of them.
 template <int D, int FMT, int NT>
-__device__ __forceinline__ void token_block(TokenState<D, NT>& me, const uint8_t* st, int key0, bool partial, bool odd,
-                                            int32_t lo, int32_t hi, int32_t lo_max, int32_t hi_min, float scale_log2,
-                                            const uint32_t (&kbyte)[2][D / 64],
-                                            uint32_t (&vbyte)[4], const uint2* qs, volatile int* poison) {
-  constexpr int KW = D / 64, VB = D / 8, NJ = D / 16;
+__device__ __forceinline__ void token_blocks(TokenState<D, NT>& me, const uint8_t* st, int key0, bool partial, int32_t lo,
+                                             int32_t hi, int32_t lo_max, int32_t hi_min, float scale_log2,
+                                             const uint2* qs, volatile int* poison) {
   using C = CacheTokenCfg<D, FMT, NT>;
-  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  constexpr int KW = D / 64, VB = D / 8, NJ = D / 16, NB = C::kSub, SW = D / kCacheGroup;
+  const int t = threadIdx.x & 3;
+  // odd: some scale's factor takes more than a shift of its byte (odd_scale); rare
+  uint32_t kbyte[NB][2][KW], vbyte[NB][4];
+  bool odd_here = false;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        kbyte[b][i][w] = st[b * C::kStageBytes + me.ks_off + i * 8 * SW + w * 2];
+        odd_here = odd_here || odd_scale<FMT>(kbyte[b][i][w]);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      vbyte[b][i] = st[b * C::kStageBytes + me.vs_off + i * 4 * SW];
+      odd_here = odd_here || odd_scale<FMT>(vbyte[b][i]);
+    }
+  }
+  const bool odd = __any_sync(0xffffffffu, odd_here);
   // S^T = K Q^T
-  float s[NT][4] = {};
-  uint32_t pf[NT][2];
+  float s[NB][NT][4] = {};
+  uint32_t pf[NB][NT][2];
 #pragma unroll
-  for (int w = 0; w < KW; ++w) {
-    uint32_t kf[2][2][4];     // [key row][operand register][step]
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const uint4 x = *reinterpret_cast<const uint4*>(st + n * 8 * D + (w == 0 ? me.k_off : me.k_off ^ 64));
-      const uint32_t f = odd ? kBf16One : kbyte[n][w] * 0x00800080u + kUnpackBias<FMT> * 0x00800080u;
-      unpack4<FMT>(x.x, kf[n][0][0], kf[n][1][0]);
-      unpack4<FMT>(x.y, kf[n][0][1], kf[n][1][1]);
-      unpack4<FMT>(x.z, kf[n][0][2], kf[n][1][2]);
-      unpack4<FMT>(x.w, kf[n][0][3], kf[n][1][3]);
+    for (int w = 0; w < KW; ++w) {
+      uint32_t kf[2][2][4];     // [key row][operand register][step]
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(st + b * C::kStageBytes + i * 8 * D +
+                                                        (w == 0 ? me.k_off : me.k_off ^ 64));
+        unpack4<FMT>(x.x, kf[i][0][0], kf[i][1][0]);
+        unpack4<FMT>(x.y, kf[i][0][1], kf[i][1][1]);
+        unpack4<FMT>(x.z, kf[i][0][2], kf[i][1][2]);
+        unpack4<FMT>(x.w, kf[i][0][3], kf[i][1][3]);
+      }
+      if (!odd) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t f = kbyte[b][i][w] * 0x00800080u + kUnpackBias<FMT> * 0x00800080u;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) kf[i][e][u] = mul_bf16x2(kf[i][e][u], f);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t f1, f2;
+          scale_factors<FMT>(kbyte[b][i][w], f1, f2);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) kf[i][e][u] = mul_bf16x2(mul_bf16x2(kf[i][e][u], f1), f2);
+        }
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) kf[n][e][u] = mul_bf16x2(kf[n][e][u], f);
+        for (int n = 0; n < NT; ++n) {
+          const uint2 q = qs[(n * NJ + w * 4 + u) * 32];
+          mma_16816(s[b][n], kf[0][0][u], kf[1][0][u], kf[0][1][u], kf[1][1][u], q.x, q.y);
+        }
     }
-    if (odd) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        uint32_t f1, f2;
-        scale_factors<FMT>(kbyte[n][w], f1, f2);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) kf[n][e][u] = mul_bf16x2(mul_bf16x2(kf[n][e][u], f1), f2);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint2 q = qs[(n * NJ + w * 4 + u) * 32];
-        mma_16816(s[n], kf[0][0][u], kf[1][0][u], kf[0][1][u], kf[1][1][u], q.x, q.y);
-      }
-  }
-  token_softmax<D, NT>(me, s, key0, partial, scale_log2, pf);
+  token_softmax<D, NT, NB>(me, s, key0, partial, scale_log2, pf);
   // O^T += V^T P^T: V rows t, 4 + t (first keys of the sum), 8 + t, 12 + t
-  uint32_t x[4][VB / 4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint8_t* src = st + ((i & 1) ? me.v_off1 : me.v_off0) + (i >> 1) * 8 * D;
-    if constexpr (D == 128) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src);
-      x[i][0] = v.x;
-      x[i][1] = v.y;
-      x[i][2] = v.z;
-      x[i][3] = v.w;
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(src);
-      x[i][0] = v.x;
-      x[i][1] = v.y;
-    }
-  }
-  if (partial) {     // what no row sees, and NaN, stay out of the product (cacheattn.cuh)
+  for (int b = 0; b < NB; ++b) {
+    uint32_t x[4][VB / 4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int key = key0 + t + 4 * i;
-      const bool seen = key >= lo && key < hi;
-      if (!seen || (vbyte[i] == kCacheNanScale && (key < lo_max || key >= hi_min))) {
-        if (seen) *poison = 1;
-        vbyte[i] = 127;
-#pragma unroll
-        for (int w = 0; w < VB / 4; ++w) x[i][w] = 0u;
+      const uint8_t* src = st + b * C::kStageBytes + ((i & 1) ? me.v_off1 : me.v_off0) + (i >> 1) * 8 * D;
+      if constexpr (D == 128) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src);
+        x[i][0] = v.x;
+        x[i][1] = v.y;
+        x[i][2] = v.z;
+        x[i][3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(src);
+        x[i][0] = v.x;
+        x[i][1] = v.y;
       }
     }
-  }
-  uint32_t f1[4], f2[4] = {kBf16One, kBf16One, kBf16One, kBf16One};
+    if (partial) {     // what no row sees, and NaN that some see, stay out of the product (cacheattn.cuh)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f1[i] = vbyte[i] * 0x00800080u + kUnpackBias<FMT> * 0x00800080u;
-  if (odd) {
+      for (int i = 0; i < 4; ++i) {
+        const int key = key0 + 16 * b + t + 4 * i;
+        const bool seen = key >= lo && key < hi;
+        if (!seen || (vbyte[b][i] == kCacheNanScale && (key < lo_max || key >= hi_min))) {
+          if (seen) *poison = 1;
+          vbyte[b][i] = 127;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) scale_factors<FMT>(vbyte[i], f1[i], f2[i]);
-  }
-  const uint32_t fa = prmt<0x5410u>(f1[0], f1[1]), fb = prmt<0x5410u>(f1[2], f1[3]);
-  const uint32_t ga = prmt<0x5410u>(f2[0], f2[1]), gb = prmt<0x5410u>(f2[2], f2[3]);
-#pragma unroll
-  for (int w = 0; w < VB / 4; ++w) {
-    uint32_t a[4] = {unpack_pair<FMT, 0>(x[0][w], x[1][w], me.flip), unpack_pair<FMT, 1>(x[0][w], x[1][w], me.flip),
-                     unpack_pair<FMT, 2>(x[0][w], x[1][w], me.flip), unpack_pair<FMT, 3>(x[0][w], x[1][w], me.flip)};
-    uint32_t c[4] = {unpack_pair<FMT, 0>(x[2][w], x[3][w], me.flip), unpack_pair<FMT, 1>(x[2][w], x[3][w], me.flip),
-                     unpack_pair<FMT, 2>(x[2][w], x[3][w], me.flip), unpack_pair<FMT, 3>(x[2][w], x[3][w], me.flip)};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      a[u] = mul_bf16x2(a[u], fa);
-      c[u] = mul_bf16x2(c[u], fb);
+          for (int w = 0; w < VB / 4; ++w) x[i][w] = 0u;
+        }
+      }
     }
+    uint32_t f1[4], f2[4] = {kBf16One, kBf16One, kBf16One, kBf16One};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f1[i] = vbyte[b][i] * 0x00800080u + kUnpackBias<FMT> * 0x00800080u;
     if (odd) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        a[u] = mul_bf16x2(a[u], ga);
-        c[u] = mul_bf16x2(c[u], gb);
-      }
+      for (int i = 0; i < 4; ++i) scale_factors<FMT>(vbyte[b][i], f1[i], f2[i]);
     }
+    const uint32_t fa = prmt<0x5410>(f1[0], f1[1]), fb = prmt<0x5410>(f1[2], f1[3]);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      mma_16816(me.o[n][2 * w], a[0], a[1], c[0], c[1], pf[n][0], pf[n][1]);
-      mma_16816(me.o[n][2 * w + 1], a[2], a[3], c[2], c[3], pf[n][0], pf[n][1]);
+    for (int w = 0; w < VB / 4; ++w) {
+      uint32_t a[4] = {unpack_pair<FMT, 0>(x[0][w], x[1][w], me.flip), unpack_pair<FMT, 1>(x[0][w], x[1][w], me.flip),
+                       unpack_pair<FMT, 2>(x[0][w], x[1][w], me.flip), unpack_pair<FMT, 3>(x[0][w], x[1][w], me.flip)};
+      uint32_t c[4] = {unpack_pair<FMT, 0>(x[2][w], x[3][w], me.flip), unpack_pair<FMT, 1>(x[2][w], x[3][w], me.flip),
+                       unpack_pair<FMT, 2>(x[2][w], x[3][w], me.flip), unpack_pair<FMT, 3>(x[2][w], x[3][w], me.flip)};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        a[u] = mul_bf16x2(a[u], fa);
+        c[u] = mul_bf16x2(c[u], fb);
+      }
+      if (odd) {
+        const uint32_t ga = prmt<0x5410>(f2[0], f2[1]), gb = prmt<0x5410>(f2[2], f2[3]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          a[u] = mul_bf16x2(a[u], ga);
+          c[u] = mul_bf16x2(c[u], gb);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_16816(me.o[n][2 * w], a[0], a[1], c[0], c[1], pf[b][n][0], pf[b][n][1]);
+        mma_16816(me.o[n][2 * w + 1], a[2], a[3], c[2], c[3], pf[b][n][0], pf[b][n][1]);
+      }
     }
   }
 }
 
-// The same for bf16 pages: ldmatrix brings both operands as the products want them, K's
+// One block of bf16 pages: ldmatrix brings both operands as the products want them, K's
 // and V's rows named as above (row i of eight is key 4 (i & 1) + i / 2), channels in
 // order.  Chunk c of a row lies at c ^ (row & 7).
 template <int D, int NT>
@@ -288,8 +340,8 @@ __device__ __forceinline__ void token_block_bf16(TokenState<D, NT>& me, const ui
   // channels; V: keys, the next channels, then keys + 8
   const int krow = key + ((lane >> 3) & 1) * 8, kc = lane >> 4;
   const int vrow = key + (lane >> 4) * 8, vc = (lane >> 3) & 1;
-  float s[NT][4] = {};
-  uint32_t pf[NT][2];
+  float s[1][NT][4] = {};
+  uint32_t pf[1][NT][2];
 #pragma unroll
   for (int u = 0; u < NJ; ++u) {
     uint32_t a0, a1, a2, a3;
@@ -297,10 +349,10 @@ __device__ __forceinline__ void token_block_bf16(TokenState<D, NT>& me, const ui
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const uint2 q = qs[(n * NJ + u) * 32];
-      mma_16816(s[n], a0, a1, a2, a3, q.x, q.y);
+      mma_16816(s[0][n], a0, a1, a2, a3, q.x, q.y);
     }
   }
-  token_softmax<D, NT>(me, s, key0, partial, scale_log2, pf);
+  token_softmax<D, NT, 1>(me, s, key0, partial, scale_log2, pf);
   if (partial) {     // what no row sees, and what is not finite of what some see, stay out (cacheattn.cuh)
 #pragma unroll 1
     for (int u = lane; u < kTokenKeys * (D / 8); u += 32) {
@@ -322,7 +374,7 @@ __device__ __forceinline__ void token_block_bf16(TokenState<D, NT>& me, const ui
     uint32_t a0, a1, a2, a3;
     ldsm_x4_trans(base + kTokenKeys * RB + vrow * RB + (((2 * j + vc) ^ key) << 4), a0, a1, a2, a3);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) mma_16816(me.o[n][j], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+    for (int n = 0; n < NT; ++n) mma_16816(me.o[n][j], a0, a1, a2, a3, pf[0][n][0], pf[0][n][1]);
   }
 }
 
@@ -376,8 +428,8 @@ __global__ void __launch_bounds__(CacheTokenCfg<D, FMT, NT>::kThreads, CacheToke
   me.v_off1 = v_place(t + 4);
   me.flip = 0x00800080u ^ (gridDim.z - 1u);   // gridDim.z is 1: a constant that stays in a register
   // scale bytes: of this thread's key and chunk, and of V row t and its channels
-  [[maybe_unused]] const int ks_off = 2 * C::kCodes + krow * (D / kCacheGroup) + (t >> 1);
-  [[maybe_unused]] const int vs_off = 2 * C::kCodes + C::kScales + t * (D / kCacheGroup) + vc * VB / kCacheGroup;
+  me.ks_off = 2 * C::kCodes + krow * (D / kCacheGroup) + (t >> 1);
+  me.vs_off = 2 * C::kCodes + C::kScales + t * (D / kCacheGroup) + vc * VB / kCacheGroup;
   // where this lane's 16-byte chunks of a block go: chunk u = lane + 32 i is row
   // u / (D / 16); i = 2, 3 (D = 128) lie eight rows further on
   [[maybe_unused]] int k_dst[2], v_dst[2];
@@ -439,14 +491,16 @@ __global__ void __launch_bounds__(CacheTokenCfg<D, FMT, NT>::kThreads, CacheToke
     left = seg_s->narrow ? max(left, static_cast<int64_t>(1)) : 0;   // warp 0 keeps the count
 
     const int rows = it.ntok * p.group;
-    // 16-key blocks [b0, b1) of the segment; this warp has every kWarps-th
+    // 16-key blocks [b0, b1) of the segment, in groups of kSub (blocks of a group that
+    // nobody sees are not loaded: whatever lies there is masked); the groups go to the
+    // warps in turn
     const int64_t ka = max(static_cast<int64_t>(it.lo), static_cast<int64_t>(it.step0 + sa) << 7);
     const int64_t kb = min(static_cast<int64_t>(it.hi), static_cast<int64_t>(it.step0 + sb) << 7);
     const int b0 = static_cast<int>(ka >> 4), b1 = sb > sa ? static_cast<int>((kb + 15) >> 4) : b0;
     const int32_t* table = p.s.page_table + static_cast<int64_t>(it.seq) * p.s.table_stride;
-    auto page_of = [&](int b) -> int32_t { return b < b1 ? table[b >> (ps - 4)] : 0; };
+    auto page_of = [&](int b) -> int32_t { return b >= b0 && b < b1 ? table[b >> (ps - 4)] : 0; };
     auto load = [&](int b, int32_t pg, int stage) {
-      if (b < b1) {
+      if (b >= b0 && b < b1) {
         const bool good = pg >= 0 && pg < p.c.num_pages;
         if (!good && lane == 0) record_error(DYNRAD_ERR_DEVICE);
         // a page outside the pool is filled with zeros
@@ -474,17 +528,22 @@ __global__ void __launch_bounds__(CacheTokenCfg<D, FMT, NT>::kThreads, CacheToke
           }
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int b = b0 + warp;
+    constexpr int SUB = C::kSub, GROUPS = C::kStages / SUB;   // groups in the ring
+    int b = b0 / SUB * SUB + warp * SUB;
     {
       int32_t pg[C::kStages];
 #pragma unroll
-      for (int s = 0; s < C::kStages; ++s) pg[s] = page_of(b + s * C::kWarps);
+      for (int s = 0; s < C::kStages; ++s) pg[s] = page_of(b + s / SUB * C::kWarps * SUB + s % SUB);
 #pragma unroll
-      for (int s = 0; s < C::kStages; ++s) load(b + s * C::kWarps, pg[s], s);
+      for (int s = 0; s < C::kStages; ++s) {
+        load(b + s / SUB * C::kWarps * SUB + s % SUB, pg[s], s);
+        if (s % SUB == SUB - 1) asm volatile("cp.async.commit_group;" ::: "memory");
+      }
     }
-    int32_t next_page = page_of(b + C::kStages * C::kWarps);
+    int32_t next_page[SUB];
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) next_page[u] = page_of(b + GROUPS * C::kWarps * SUB + u);
 
     // Q's operands: query row 8 n + g, step u.  8-bit: of chunk t + 4 (u / 4) the channels
     // of word u % 4; bf16: channels 16 u + 2 t and 16 u + 8 + 2 t
@@ -519,37 +578,25 @@ __global__ void __launch_bounds__(CacheTokenCfg<D, FMT, NT>::kThreads, CacheToke
 
     int stage = 0;
 #pragma unroll 1
-    for (; b < b1; b += C::kWarps) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
+    for (; b < b1; b += C::kWarps * SUB) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(GROUPS - 1) : "memory");
       __syncwarp();
       const uint8_t* st = ring + stage * C::kStageBytes;
       const int key0 = b << 4;
-      const bool partial = key0 < it.lo_max || key0 > it.hi_min - 16;
-      if constexpr (C::kRaw) {
-        uint32_t kbyte[2][KW], vbyte[4];
-        bool odd = false;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            kbyte[n][w] = st[ks_off + n * 8 * (D / kCacheGroup) + w * 2];
-            odd = odd || odd_scale<FMT>(kbyte[n][w]);
-          }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          vbyte[i] = st[vs_off + i * 4 * (D / kCacheGroup)];
-          odd = odd || odd_scale<FMT>(vbyte[i]);
-        }
-        token_block<D, FMT, NT>(me, st, key0, partial, __any_sync(0xffffffffu, odd), it.lo, it.hi, it.lo_max,
-                                it.hi_min, p.scale_log2, kbyte, vbyte, q_s + lane, poison);
-      } else {
+      const bool partial = key0 < it.lo_max || key0 > it.hi_min - kTokenKeys * SUB;
+      if constexpr (C::kRaw)
+        token_blocks<D, FMT, NT>(me, st, key0, partial, it.lo, it.hi, it.lo_max, it.hi_min, p.scale_log2, q_s + lane,
+                                 poison);
+      else
         token_block_bf16<D, NT>(me, st, key0, partial, it.lo, it.hi, it.lo_max, it.hi_min, p.scale_log2, q_s + lane,
                                 poison);
-      }
       __syncwarp();      // every lane has read the stage
-      load(b + C::kStages * C::kWarps, next_page, stage);
-      next_page = page_of(b + (C::kStages + 1) * C::kWarps);
-      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) load(b + GROUPS * C::kWarps * SUB + u, next_page[u], stage + u);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) next_page[u] = page_of(b + (GROUPS + 1) * C::kWarps * SUB + u);
+      stage = stage + SUB == C::kStages ? 0 : stage + SUB;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
