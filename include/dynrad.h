@@ -558,8 +558,9 @@ int dynrad_cache_read(const dynrad_kv_cache *cache, const dynrad_seqs *seqs,
  *   frame >= 1, window w  of those the last w frames, its own among them
  * and over what it sees
  *   o   = sum softmax(scale * q.k) v,   lse = ln sum exp(scale * q.k)
- * with the tensor cores (tcgen05, bf16 operands, fp32 accumulation, P rounded to
- * bf16) and an fp32 softmax.  A row that sees nothing, or whose logits are all
+ * with the tensor cores (bf16 operands, fp32 accumulation, P rounded to bf16;
+ * tcgen05, or warp-level products where a call has few rows to a K / V head) and
+ * an fp32 softmax.  A row that sees nothing, or whose logits are all
  * -inf, gives o = 0 and lse = -inf.  What a row does not see cannot reach it,
  * whatever it holds (NaN, infinity, memory never written).  lse is that of
  * dynrad_sparse_attn, so parts of one row's keys can be joined by it.
