@@ -696,6 +696,11 @@ def dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens=None, head_m
     return k, v
 
 
+def dynrad_cache_attn_workspace_bytes(cache, num_seqs, num_tokens, heads) -> int:
+    """Bytes of dynrad_cache_attn's workspace (0 if the call can not be made)."""
+    return int(lib().dynrad_cache_attn_workspace_bytes(ctypes.byref(cache.c), num_seqs, num_tokens, heads))
+
+
 def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, scale=0.0, out=None, lse=None,
                       workspace=None, stream=None):
     """Attention of the new tokens q (bf16 [T, heads, D], heads a multiple of the
@@ -703,7 +708,9 @@ def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, s
     token sees its whole sequence; frame >= 1: up to the end of its own frame of
     that many positions (1: token-causal); window >= 1: of those the last
     ``window`` frames.  Returns (o bf16 [T, heads, D], laid out as q, and lse fp32 [heads, T]); rows
-    behind cu_seq[-1] are left as they are."""
+    behind cu_seq[-1] are left as they are.  ``workspace``: a contiguous tensor of
+    dynrad_cache_attn_workspace_bytes bytes or more, 256-byte aligned, that no other
+    call in flight uses; None allocates one."""
     if stream is not None:    # what is allocated here belongs to that stream too
         with torch.cuda.stream(stream):
             return dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame, window, scale, out, lse, workspace)
@@ -721,14 +728,17 @@ def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, s
     elif (lse.dtype != torch.float32 or lse.shape != (H, T) or not lse.is_contiguous() or
           lse.get_device() != cache.device_index):
         raise ValueError("lse must be a contiguous fp32 [heads, T] tensor")
+    if workspace is not None and (workspace.get_device() != cache.device_index or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and on the cache's device")
     st = _cache_stream(cache)
     L = lib()
     if workspace is None:
-        need = L.dynrad_cache_attn_workspace_bytes(ctypes.byref(cache.c), sq.num_seqs, T, H)
+        need = dynrad_cache_attn_workspace_bytes(cache, sq.num_seqs, T, H)
         if need == 0:
             raise DynradError(DYNRAD_ERR_INVALID_ARG, "dynrad_cache_attn_workspace_bytes")
         workspace = q.new_empty(need, dtype=torch.uint8)
     _check(L.dynrad_cache_attn(ctypes.byref(cache.c), ctypes.byref(sq), q.data_ptr(), qt, qh, H, int(frame),
                                int(window), float(scale), o.data_ptr(), ot, oh, lse.data_ptr(),
-                               workspace.data_ptr(), workspace.numel(), st), "dynrad_cache_attn")
+                               workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
+           "dynrad_cache_attn")
     return o, lse

@@ -1250,8 +1250,8 @@ int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, i
   pl->tile_tokens = 128 / pl->group;
   // Sequences of 8 or 16 rows on average at most: the kernel of single tokens, else the
   // tensor-core tiles of 128 rows.  Measured at 8 rows (tiles / this, us): three
-  // sequences of 131,072 keys in e4m3 333 / 182, in bf16 252 / 252; a ragged batch of 64
-  // up to 16,000 keys in int8 486 / 212, in bf16 383 / 294; one token over 777 keys in
+  // sequences of 131,072 keys in e4m3 333 / 168, in bf16 252 / 252; a ragged batch of 64
+  // up to 16,000 keys in int8 486 / 189, in bf16 383 / 294; one token over 777 keys in
   // bf16 18.9 / 10.9 on the GPU.  Beyond 16 rows its products would repeat the unpacking.
   pl->token_tiles = 0;
   for (int nt = 2; nt >= 1; --nt)

@@ -144,6 +144,18 @@ def test_binding_checks_tensors():
             raise AssertionError(i)
 
 
+def test_binding_checks_the_workspace():
+    i32 = torch.int32
+    kv = torch.zeros((5, 2, 16, 64), dtype=torch.bfloat16)
+    cache = abi.KVCache(kv, kv.clone())
+    q = torch.zeros((9, 4, 64), dtype=torch.bfloat16)
+    seqs = torch.zeros((3, 4), dtype=i32), torch.zeros(4, dtype=i32), torch.zeros(3, dtype=i32)
+    need = abi.dynrad_cache_attn_workspace_bytes(cache, 3, 9, 4)
+    assert need > 0 and abi.dynrad_cache_attn_workspace_bytes(cache, 3, 9, 3) == 0
+    with pytest.raises(ValueError, match="workspace"):
+        abi.dynrad_cache_attn(q, cache, *seqs, workspace=torch.zeros(2 * need, dtype=torch.uint8)[::2])
+
+
 # ------------------------------------------------------------------ the oracle's pins --
 def test_oracle_e4m3_is_torchs():
     y = torch.cat([torch.linspace(-448, 448, 40001), torch.logspace(-12, 8.8, 20001, base=2),

@@ -479,3 +479,29 @@ def test_calls_on_other_streams_and_captured():
                     x[w.cu_np[s] + lens[s] - 1] = 0.0
         check_attention(out, lse, nq, *([x[w.cu_np[s]:w.cu_np[s] + now.lens[s]] for s in range(3)] for x in kept),
                         now, 1, 0)
+
+
+@pytest.mark.parametrize("ns,lens,group", [([1], [4000], 8), ([1, 2, 1], [3000, 1200, 15], 8), ([200, 1], [2500, 90], 3),
+                                           ([40], [1100], 4)])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_one_workspace_for_calls_in_turn(ns, lens, group, fmt):
+    """The caller's workspace: whatever it holds, and whichever call used it before."""
+    b = Batch(ns, lens, 64, seed=3)
+    g = gen(5)
+    c, _, _ = filled_cache(b, 2, 128, fmt, g)
+    q = torch.randn((b.tokens, 2 * group, 128), generator=g, device="cuda").bfloat16()
+    need = abi.dynrad_cache_attn_workspace_bytes(c, len(ns), b.tokens, 2 * group)
+    ws = torch.full((need // 4 + 64,), float("nan"), device="cuda")
+    for frame in (1, 0):
+        o_ref, lse_ref = abi.dynrad_cache_attn(q, c, *b.call(), frame=frame)
+        for _ in range(2):
+            o, lse = abi.dynrad_cache_attn(q, c, *b.call(), frame=frame, workspace=ws)
+            assert torch.equal(o, o_ref) and torch.equal(lse, lse_ref)
+    torch.cuda.synchronize()
+    check_device_status()
+    with pytest.raises(abi.DynradError):
+        abi.dynrad_cache_attn(q, c, *b.call(), workspace=ws[:need // 4 - 1])
+    with pytest.raises(abi.DynradError):
+        abi.dynrad_cache_attn(q, c, *b.call(), workspace=ws[1:])
+    with pytest.raises(ValueError):
+        abi.dynrad_cache_attn(q, c, *b.call(), workspace=ws.cpu())
