@@ -108,7 +108,7 @@ struct CacheAttnParams {
   float scale_log2;
   float* part_o;                 // [2 * CTAs][rows][D]
   float2* part_ml;               // [2 * CTAs][rows]
-  int4* part_desc;               // [2 * CTAs]: place, K / V head, kPart*
+  int4* part_desc;               // [2 * CTAs]: first token, K / V head, kPart*, tokens
   uint64_t wait_ns;
   int32_t stall_step;            // as in AttnParams
 };
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
         sg.part = whole ? -1 : (sg.sa > 0 ? 0 : 1);
         if (!whole && lane == 0)
           p.part_desc[2 * blockIdx.x + sg.part] =
-              make_int4(place, head, sg.sb == sg.it.steps ? kPartLast : kPartOpen, 0);
+              make_int4(sg.it.tok0, head, sg.sb == sg.it.steps ? kPartLast : kPartOpen, sg.it.ntok);
         sg.narrow = QT == 1 || sg.it.ntok <= p.tile_tokens;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -1068,52 +1068,52 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
 // first part CTA x of that launch wrote (slot 1), followed by slot 0 of the CTAs
 // after it up to the last part.  Weights 2^(m_i - max m), sums in order of the parts.
 // A row belongs to D / 4 lanes: they weigh its parts side by side, then each adds up
-// its four channels, eight parts' loads in flight (74 parts of 8 rows: 21 -> 6 us
-// against one part after the other).
+// its four channels, N parts' loads in flight.  Chains of loads bound it: descriptors
+// (32 at a look, with all that is needed of the item), then parts.  N = 8 for few rows
+// (74 parts of 8 rows: 21 us with one load at a time, 6 so); chunks' items have many
+// rows of few parts and take N = 4, whose registers let five CTAs on an SM.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinMost = 3 * kCacheMaxCtas;     // parts of an item, at most one for each CTA
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAttnParams p, int item_tokens,
-                                                                  int rows_per_part, int ctas) {
+template <int D, int N>
+__global__ void __launch_bounds__(kJoinThreads, N == 8 ? 3 : 5) cache_join_kernel(const CacheAttnParams p,
+                                                                                  int rows_per_part, int ctas) {
   constexpr int L = D / 4;        // lanes a row
   constexpr int R = kJoinThreads / L;
   __shared__ float weights[R][kJoinMost];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int x = blockIdx.x;
-  const int4 d0 = p.part_desc[2 * x + 1];
-  if (d0.z != kPartOpen) return;
-  // the first later part that is not open ends the item; 32 descriptors at a look (one
-  // after the other: 3 us more at 19 parts)
-  const int lane = threadIdx.x & 31;
-  int parts = 1;
+  const int x = blockIdx.x, lane = threadIdx.x & 31;
+  int4 d = make_int4(0, 0, kPartNone, 0);
+  if (x + lane < ctas) d = p.part_desc[2 * (x + lane) + (lane == 0 ? 1 : 0)];
+  if (__shfl_sync(0xffffffffu, d.z, 0) != kPartOpen) return;
+  const int tok0 = __shfl_sync(0xffffffffu, d.x, 0), kv_head = __shfl_sync(0xffffffffu, d.y, 0);
+  const int ntok = __shfl_sync(0xffffffffu, d.w, 0);
+  // the first later part that is not open ends the item
+  int parts = 0;
   while (true) {
-    const int at = x + parts + lane;
-    const int z = at < ctas ? p.part_desc[2 * at].z : kPartNone;
-    const uint32_t stop = __ballot_sync(0xffffffffu, z != kPartOpen);
-    if (stop == 0u) {
-      parts += 32;
-      continue;
+    const uint32_t stop = __ballot_sync(0xffffffffu, d.z != kPartOpen);
+    if (stop != 0u) {
+      const int first = __ffs(stop) - 1;
+      if (__shfl_sync(0xffffffffu, d.z, first) == kPartNone) return;   // a launch that gave up (recorded)
+      parts += first + 1;
+      break;
     }
-    const int first = __ffs(stop) - 1;
-    if (__shfl_sync(0xffffffffu, z, first) == kPartNone) return;   // a launch that gave up (recorded)
-    parts += first + 1;
-    break;
+    parts += 32;
+    d.z = x + parts + lane < ctas ? p.part_desc[2 * (x + parts + lane)].z : kPartNone;
   }
-  const CacheItem it = find_item(p, item_tokens, d0.x);
   // row = tile * 128 + token of the tile * group + head of the group
-  const int tile_rows = p.tile_tokens * p.group, rows = it.ntok * p.group;
+  const int tile_rows = p.tile_tokens * p.group, rows = ntok * p.group;
   const int c = threadIdx.x % L, slot = threadIdx.x / L;
   const uint32_t lanes = L == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
   float* w = weights[slot];
   for (int i = blockIdx.y * R + slot; i < rows; i += gridDim.y * R) {
     const int tile = i / tile_rows, row = tile * 128 + (i - tile * tile_rows);
     auto at = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * x + 1 : 2 * (x + k)) * rows_per_part + row; };
-    // the first eight parts' channels do not wait for the weights
-    float4 v[8];
+    // the first parts' channels do not wait for the weights
+    float4 v[N];
     auto fetch = [&](int k0) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
+      for (int u = 0; u < N; ++u)
         if (k0 + u < parts) v[u] = __ldcs(reinterpret_cast<const float4*>(p.part_o + at(k0 + u) * D) + c);
     };
     fetch(0);
@@ -1131,10 +1131,10 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
     for (int o = L / 2; o > 0; o >>= 1) l += __shfl_xor_sync(lanes, l, o);
     __syncwarp(lanes);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < parts; k0 += 8) {
+    for (int k0 = 0; k0 < parts; k0 += N) {
       if (k0 > 0) fetch(k0);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < N; ++u) {
         const float f = k0 + u < parts ? w[k0 + u] : 0.f;
         if (f == 0.f) continue;
         o.x = fmaf(v[u].x, f, o.x);
@@ -1145,8 +1145,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
     }
     __syncwarp(lanes);
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t token = it.tok0 + i / p.group;
-    const int head = d0.y * p.group + i % p.group;
+    const int64_t token = tok0 + i / p.group;
+    const int head = kv_head * p.group + i % p.group;
     *reinterpret_cast<uint2*>(p.o + token * p.o_token + head * p.o_head + c * 4) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     if (c == 0)

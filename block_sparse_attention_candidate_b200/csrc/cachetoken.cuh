@@ -463,7 +463,6 @@ __global__ void __launch_bounds__(CacheTokenCfg<D, FMT, NT>::kThreads, CacheToke
         } else {
           left = 0;
         }
-        const int at = place;
         if (++place == p.slots) {
           place = 0;
           if (++head == p.c.heads) left = 0;
@@ -473,7 +472,7 @@ __global__ void __launch_bounds__(CacheTokenCfg<D, FMT, NT>::kThreads, CacheToke
           sg.part = sg.sa > 0 ? 0 : 1;
           if (lane == 0)
             p.part_desc[2 * blockIdx.x + sg.part] =
-                make_int4(at, sg.head, sg.sb == sg.it.steps ? kPartLast : kPartOpen, 0);
+                make_int4(sg.it.tok0, sg.head, sg.sb == sg.it.steps ? kPartLast : kPartOpen, sg.it.ntok);
         }
         sg.end = use ? 0 : 1;
         if (use || left <= 0) break;

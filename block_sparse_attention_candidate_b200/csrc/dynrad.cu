@@ -1337,7 +1337,7 @@ int launch_cache_token(const CacheAttnParams& p, int tiles, int ctas, cudaStream
   return tiles == 1 ? launch_cache_token<D, FMT, 1>(p, ctas, st) : launch_cache_token<D, FMT, 2>(p, ctas, st);
 }
 
-template <int D>
+template <int D, int N>
 int launch_cache_join(const CacheAttnParams& p, const CachePlan& pl, int ctas, cudaStream_t st) {
   // the launch overlaps the end of the attention; the kernel waits for all of it
   const int per_cta = kJoinThreads / (D / 4);
@@ -1351,7 +1351,7 @@ int launch_cache_join(const CacheAttnParams& p, const CachePlan& pl, int ctas, c
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, p, pl.item_tokens, pl.part_rows, ctas) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D, N>, p, pl.part_rows, ctas) != cudaSuccess)
     return DYNRAD_ERR_CUDA;
   return launch_status();
 }
@@ -1437,5 +1437,7 @@ extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs
 #undef DYNRAD_CACHE_F
   }
   if (rc != DYNRAD_OK || !pl.split) return rc;
-  return cache->dim == 128 ? launch_cache_join<128>(p, pl, ctas, st) : launch_cache_join<64>(p, pl, ctas, st);
+  if (pl.token_tiles > 0)
+    return cache->dim == 128 ? launch_cache_join<128, 8>(p, pl, ctas, st) : launch_cache_join<64, 8>(p, pl, ctas, st);
+  return cache->dim == 128 ? launch_cache_join<128, 4>(p, pl, ctas, st) : launch_cache_join<64, 4>(p, pl, ctas, st);
 }
