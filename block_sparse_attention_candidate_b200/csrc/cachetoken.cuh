@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(CacheTokenCfg<D, FMT, NT>::kThreads, CacheToke
       CacheSeg sg;
       for (;;) {
         sg.it = find_item(p, item_tokens, place);
-        const int32_t units = item_units(sg.it);
+        const int32_t units = item_units(p, item_tokens, sg.it);
         sg.head = head;
         sg.sa = 0;
         sg.sb = sg.it.steps;
@@ -455,8 +455,8 @@ __global__ void __launch_bounds__(CacheTokenCfg<D, FMT, NT>::kThreads, CacheToke
         if (p.split) {
           const int64_t take = min(left, static_cast<int64_t>(units) - off);
           if (units > 0) {
-            sg.sa = static_cast<int32_t>(max(off - kCacheItemCost, static_cast<int64_t>(0)));
-            sg.sb = static_cast<int32_t>(max(off + take - kCacheItemCost, static_cast<int64_t>(0)));
+            sg.sa = unit_step(p, item_tokens, sg.it, off);
+            sg.sb = unit_step(p, item_tokens, sg.it, off + take);
             left -= take;
           }
           off = 0;
