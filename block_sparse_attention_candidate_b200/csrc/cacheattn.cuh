@@ -50,11 +50,12 @@
 //
 // Every wait is bounded (common.cuh).
 //
-// Measured: 1560 tokens over 18720 keys of 12 heads, bf16, 238 us (754 TFLOP/s; tensor
-// pipe 43 % of the time, exponentials 41 %); over 32760 keys of 40 heads, e4m3, 1460 us
-// (717 TFLOP/s); 1536 tokens over 132000 keys, bf16, 960-985 TFLOP/s.  A step of 128 keys
-// of two tiles takes about 4150 cycles, bound by the chain S -> softmax -> P V; e4m3
-// about 5500, its unpacking sharing issue slots and ALU with the softmax.
+// Measured: 1560 tokens over 18720 keys of 12 heads, bf16, 219 us (817 TFLOP/s) and
+// over 32760 keys of 40 heads, e4m3, 1400-1460 us (715-745 TFLOP/s); 1536 tokens over
+// 132000 keys, bf16, 960-985 TFLOP/s.  A step of 128 keys of two tiles takes about 4300
+// cycles (tensor pipe 43 % busy, exponentials 41 %), bound by the chain S -> softmax ->
+// P V of each tile; e4m3 about 5500, its unpacking sharing issue slots and ALU with the
+// softmax.
 #pragma once
 
 #include "attention.cuh"

@@ -36,8 +36,8 @@
 // runs twelve warps: two CTAs of six, or three of four (8-bit, NT = 1).
 //
 // Measured on 8 K / V heads of D 128 (times of the launch and its join):
-//   3 x 131072 keys, 64 heads: e4m3 168 us (4.9 TB/s), int8 154 (5.4), bf16 252 (6.4);
-//   64 sequences of up to 16000 keys, 32 heads: int8 189 us (5.2), bf16 295 (6.4).
+//   3 x 131072 keys, 64 heads: e4m3 166 us (5.0 TB/s), int8 152 (5.5), bf16 243-252 (6.4-6.6);
+//   64 sequences of up to 16000 keys, 32 heads: int8 184 us (5.3), bf16 295 (6.4).
 // 8-bit pages are bound by issue (unpacking a byte and scaling it), not by HBM.  Pairs
 // of blocks share the softmax step's shuffles and votes: with single blocks and eight
 // warps in each of three CTAs (80 registers) the 8-bit times were 182, 170 and 212 us;
