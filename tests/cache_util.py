@@ -25,7 +25,7 @@ class Batch:
 
     def __init__(self, ns, lens, page, seed=0, tail=0, pad_cols=1, lead_pages=0, keys=0, skip=0):
         """keys: what the table's rows can hold at least (the library cuts items into
-        parts only where that is over 1024); skip: rows before the first sequence's."""
+        parts where that is over 1024, chunks from 512 on); skip: rows before the first sequence's."""
         rng = np.random.default_rng(seed)
         self.ns, self.lens, self.page = list(ns), list(lens), page
         used = [-(-n // page) for n in lens]
