@@ -221,6 +221,15 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t x) {
   return ((x & 0x7f80u) == 0x7f80u ? 0u : x & 0xffffu) | ((x & 0x7f800000u) == 0x7f800000u ? 0u : x & 0xffff0000u);
 }
 
+// Weight of what was summed under the maximum m (log2 units) where the largest of all
+// is `most`; 1 where nobody met a logit over -inf.  It may underflow to 0, and such a
+// share is added like any other: where it is finite that adds nothing, and its NaN or
+// infinity (of a key or V that the row sees) comes through as it does when the same keys
+// are summed in one.
+__device__ __forceinline__ float join_weight(float m, float most) {
+  return most == -INFINITY ? 1.f : ex2_approx(m - most);
+}
+
 // Units of the launch's longest steps, and of an item's.
 __device__ __forceinline__ int32_t longest_step(const CacheAttnParams& p, int item_tokens) {
   return item_tokens > p.tile_tokens ? kWideUnits : 1;
@@ -651,8 +660,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
             have1 = true;
             const float2 b = ml[t];
             const float m = fmaxf(m_used, b.x);
-            w0 = m_used == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_approx(m_used - m);
-            w1 = b.x == -INFINITY ? (b.y == 0.f ? 0.f : 1.f) : ex2_approx(b.x - m);
+            w0 = join_weight(m_used, m);
+            w1 = join_weight(b.x, m);
             l = l * w0 + b.y * w1;
             m_used = m;
           }
@@ -679,13 +688,12 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
               tmem_wait_ld();
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = have && w0 != 0.f ? __uint_as_float(r[i]) * w0 : 0.f;
+            for (int i = 0; i < 32; ++i) x[i] = have ? __uint_as_float(r[i]) * w0 : 0.f;
             if (have1) {
               tmem_ld32(taddr + lane_base + 128u + c * 32, r);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (w1 != 0.f) x[i] = fmaf(__uint_as_float(r[i]), w1, x[i]);
+              for (int i = 0; i < 32; ++i) x[i] = fmaf(__uint_as_float(r[i]), w1, x[i]);
             }
           }
           if (poisoned && valid) {
@@ -1146,9 +1154,9 @@ __global__ void __launch_bounds__(kJoinThreads, N == 8 ? 3 : 5) cache_join_kerne
     for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
     for (int k = c; k < parts; k += L) {
       const float2 b = p.part_ml[at(k)];
-      const float f = b.x == -INFINITY ? (b.y == 0.f ? 0.f : 1.f) : ex2_approx(b.x - m);
+      const float f = join_weight(b.x, m);
       w[k] = f;
-      l = f == 0.f ? l : fmaf(b.y, f, l);
+      l = fmaf(b.y, f, l);
     }
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) l += __shfl_xor_sync(lanes, l, o);
@@ -1158,8 +1166,8 @@ __global__ void __launch_bounds__(kJoinThreads, N == 8 ? 3 : 5) cache_join_kerne
       if (k0 > 0) fetch(k0);
 #pragma unroll
       for (int u = 0; u < N; ++u) {
-        const float f = k0 + u < parts ? w[k0 + u] : 0.f;
-        if (f == 0.f) continue;
+        if (k0 + u >= parts) continue;
+        const float f = w[k0 + u];
         o.x = fmaf(v[u].x, f, o.x);
         o.y = fmaf(v[u].y, f, o.y);
         o.z = fmaf(v[u].z, f, o.z);

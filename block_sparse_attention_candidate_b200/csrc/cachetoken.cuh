@@ -634,8 +634,7 @@ __global__ void __launch_bounds__(CacheTokenCfg<D, FMT, NT>::kThreads, CacheToke
 #pragma unroll
       for (int w = 0; w < C::kWarps; ++w) {
         const float2 x = ml[w * C::kRows + r];
-        const float f = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2_approx(x.x - mm);
-        if (f == 0.f) continue;
+        const float f = join_weight(x.x, mm);
         const float4 v = reinterpret_cast<const float4*>(token_smem + w * C::kRingBytes + r * (D * 4))[c];
         ll = fmaf(x.y, f, ll);
         a.x = fmaf(v.x, f, a.x);

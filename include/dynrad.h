@@ -562,7 +562,9 @@ int dynrad_cache_read(const dynrad_kv_cache *cache, const dynrad_seqs *seqs,
  * tcgen05, or warp-level products where a call has few rows to a K / V head) and
  * an fp32 softmax.  A row that sees nothing, or whose logits are all
  * -inf, gives o = 0 and lse = -inf.  What a row does not see cannot reach it,
- * whatever it holds (NaN, infinity, memory never written).  lse is that of
+ * whatever it holds (NaN, infinity, memory never written).  What it sees does, under
+ * any weight: a NaN in K makes its o and lse NaN, a NaN or infinity in V its o's
+ * channel NaN or infinite, though the weight underflow.  lse is that of
  * dynrad_sparse_attn, so parts of one row's keys can be joined by it.  The sum
  * over v is divided at the end and its weights reach 2^8, so the magnitudes of v
  * that a row sees must add up to less than 2^120 in each channel.
