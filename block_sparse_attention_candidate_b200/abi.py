@@ -708,7 +708,7 @@ def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, s
     token sees its whole sequence; frame >= 1: up to the end of its own frame of
     that many positions (1: token-causal); window >= 1: of those the last
     ``window`` frames.  Returns (o bf16 [T, heads, D], laid out as q, and lse fp32 [heads, T]); rows
-    behind cu_seq[-1] are left as they are.  ``workspace``: a contiguous tensor of
+    behind cu_seq[-1] are left as they are.  ``out`` must not overlap q.  ``workspace``: a contiguous tensor of
     dynrad_cache_attn_workspace_bytes bytes or more, 256-byte aligned, that no other
     call in flight uses; None allocates one."""
     if stream is not None:    # what is allocated here belongs to that stream too

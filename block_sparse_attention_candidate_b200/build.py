@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdynrad.so")
 SOURCES = ["dynrad.cu", "host_path.cu"]
 HEADERS = ["common.cuh", "candidates.cuh", "select.cuh", "attention.cuh", "sampling.cuh", "dyntok.cuh", "backward.cuh", "warp_mma.cuh",
-           "kvcache.cuh", "cacheattn.cuh", "cachetoken.cuh", "tma2d.cuh", "optin.h"]
+           "kvcache.cuh", "cacheattn.cuh", "cachetoken.cuh", "tma2d.cuh", "rows.h", "optin.h"]
 
 
 def nvcc_path() -> str:

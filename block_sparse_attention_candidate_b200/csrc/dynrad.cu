@@ -22,6 +22,7 @@
 #include "common.cuh"
 #include "backward.cuh"
 #include "optin.h"
+#include "rows.h"
 #include "dyntok.cuh"
 #include "kvcache.cuh"
 #include "sampling.cuh"
@@ -1213,6 +1214,11 @@ extern "C" int dynrad_cache_read(const dynrad_kv_cache* cache, const dynrad_seqs
   if (p.s.num_seqs == 0 || p.s.num_tokens == 0) return DYNRAD_OK;
   if (bad_rows(k, k_token_stride, k_head_stride) || bad_rows(v, v_token_stride, v_head_stride))
     return DYNRAD_ERR_INVALID_ARG;
+  const int64_t T = p.s.num_tokens, H = cache->heads;
+  if (rows_meet_own(k_token_stride, k_head_stride, T, H, cache->dim) ||
+      rows_meet_own(v_token_stride, v_head_stride, T, H, cache->dim) ||
+      rows_meet(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, T, H, cache->dim))
+    return DYNRAD_ERR_INVALID_ARG;
   p.k_out = static_cast<__nv_bfloat16*>(k);
   p.v_out = static_cast<__nv_bfloat16*>(v);
   p.k_token = k_token_stride;
@@ -1392,6 +1398,9 @@ extern "C" int dynrad_cache_attn(const dynrad_kv_cache* cache, const dynrad_seqs
   if ((heads > 1 && q_head_stride == 0) || (p.s.num_tokens > 1 && q_token_stride == 0)) return DYNRAD_ERR_INVALID_ARG;
   if (workspace_bytes < dynrad_cache_attn_workspace_bytes(cache, p.s.num_seqs, p.s.num_tokens, heads))
     return DYNRAD_ERR_CAPACITY;
+  if (rows_meet_own(o_token_stride, o_head_stride, p.s.num_tokens, heads, cache->dim) ||
+      rows_meet(q, q_token_stride, q_head_stride, o, o_token_stride, o_head_stride, p.s.num_tokens, heads, cache->dim))
+    return DYNRAD_ERR_INVALID_ARG;
   const float sc = scale == 0.0f ? 1.0f / std::sqrt(static_cast<float>(cache->dim)) : scale;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = static_cast<const __nv_bfloat16*>(q);

@@ -541,7 +541,8 @@ int dynrad_cache_write(const dynrad_kv_cache *cache, const dynrad_seqs *seqs,
  * The reverse: what the cache holds at the call's tokens' positions, as bf16
  * (exactly what is stored).  With one sequence, cu_seq = {0, kv_len} and
  * head-major strides it gives the [1, H, N, D] tensors of dynrad_select_blocks
- * and dynrad_sparse_attn.  Arguments as above; k and v are written.
+ * and dynrad_sparse_attn.  Arguments as above; k and v are written, and no two rows
+ * of them may share memory (DYNRAD_ERR_INVALID_ARG; as for o below).
  */
 int dynrad_cache_read(const dynrad_kv_cache *cache, const dynrad_seqs *seqs,
                       void *k, int64_t k_token_stride, int64_t k_head_stride,
@@ -570,13 +571,16 @@ int dynrad_cache_read(const dynrad_kv_cache *cache, const dynrad_seqs *seqs,
  * that a row sees must add up to less than 2^120 in each channel.
  *
  *   q, o          DEVICE bf16, 16-byte aligned; strides in elements, multiples of
- *                 8, as in dynrad_cache_write; o must not overlap q
+ *                 8, as in dynrad_cache_write.  No row of o may share memory
+ *                 with another or with one of q; o may lie between q's rows
+ *                 (two slices of one tensor) with the same strides only
  *   heads         query heads, a multiple of cache->heads, at most 128 to each
  *   scale         logit scale, a normal number; 0 means 1/sqrt(dim)
- *   lse           DEVICE fp32 [heads, num_tokens]
+ *   lse           DEVICE fp32 [heads, num_tokens], apart from q and o
  *   workspace     DEVICE, 256-byte aligned, at least
  *                 dynrad_cache_attn_workspace_bytes(...) bytes (0 if it can not
- *                 be sized); its contents do not matter and none are kept.
+ *                 be sized), apart from the other operands; its contents do not
+ *                 matter and none are kept.
  *                 Calls that overlap on the GPU need a workspace each.
  * Errors: DYNRAD_ERR_INVALID_ARG / UNSUPPORTED / CAPACITY before any launch.
  */
