@@ -58,6 +58,7 @@ EXPORTED = (
 
 CACHE_FORMATS = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, torch.int8: 2}
 CACHE_GROUP = 32   # channels under one scale of the 8-bit formats
+INT32_MAX = 2 ** 31 - 1   # ctypes takes larger numbers modulo 2^32 without a word
 
 
 class DynradGeom(ctypes.Structure):
@@ -608,6 +609,8 @@ def _cache_seqs(cache, page_table, cu_seq, kv_len, num_tokens) -> DynradSeqs:
         raise ValueError(f"page_table has {S} rows: cu_seq needs {S + 1} entries and kv_len {S}")
     if page_table.get_device() != dev or cu_seq.get_device() != dev or kv_len.get_device() != dev:
         raise ValueError("page_table, cu_seq and kv_len must be on the cache's device")
+    if max(S, cols, num_tokens) > INT32_MAX:
+        raise ValueError("a call takes fewer than 2^31 sequences, pages a sequence and tokens")
     stride, col = page_table.stride()
     if S <= 1:
         stride = cols
@@ -698,6 +701,8 @@ def dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens=None, head_m
 
 def dynrad_cache_attn_workspace_bytes(cache, num_seqs, num_tokens, heads) -> int:
     """Bytes of dynrad_cache_attn's workspace (0 if the call can not be made)."""
+    if max(num_seqs, num_tokens, heads) > INT32_MAX or min(num_seqs, num_tokens, heads) < 0:
+        return 0
     return int(lib().dynrad_cache_attn_workspace_bytes(ctypes.byref(cache.c), num_seqs, num_tokens, heads))
 
 
@@ -717,6 +722,9 @@ def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, s
     if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache.heads:
         raise ValueError("q must be [T, heads, D] with a multiple of the cache's heads")
     T, H, D = q.shape
+    frame, window = int(frame), int(window)
+    if max(frame, window) > INT32_MAX or min(frame, window) < -INT32_MAX:     # negative ones the library refuses
+        raise ValueError("frame and window must lie in 0 .. 2^31 - 1")
     sq = _cache_seqs(cache, page_table, cu_seq, kv_len, T)
     qt, qh = _cache_rows(cache, "q", q, H)
     if (T > 1 and qt == 0) or (H > 1 and qh == 0):
@@ -737,8 +745,8 @@ def dynrad_cache_attn(q, cache, page_table, cu_seq, kv_len, frame=1, window=0, s
         if need == 0:
             raise DynradError(DYNRAD_ERR_INVALID_ARG, "dynrad_cache_attn_workspace_bytes")
         workspace = q.new_empty(need, dtype=torch.uint8)
-    _check(L.dynrad_cache_attn(ctypes.byref(cache.c), ctypes.byref(sq), q.data_ptr(), qt, qh, H, int(frame),
-                               int(window), float(scale), o.data_ptr(), ot, oh, lse.data_ptr(),
+    _check(L.dynrad_cache_attn(ctypes.byref(cache.c), ctypes.byref(sq), q.data_ptr(), qt, qh, H, frame,
+                               window, float(scale), o.data_ptr(), ot, oh, lse.data_ptr(),
                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
            "dynrad_cache_attn")
     return o, lse
