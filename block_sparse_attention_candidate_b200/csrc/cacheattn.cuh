@@ -24,7 +24,8 @@
 // max and sum, fp32) goes to the workspace, and cache_join_kernel joins the parts
 // in order of their keys, so results repeat bit for bit.  Lengths are known on the device only,
 // so each CTA finds its run by itself: a scan over the items at its start.
-// With many items (split = false) a CTA takes one, the longest first.
+// With many items (split = false) a CTA takes one, from the last place on: of a
+// sequence the items that see most come first, between sequences the order says nothing.
 //
 // Warp roles:
 //   warps 0-3, 4-7  softmax of tile 0 / 1: thread = row = TMEM lane; as in the
@@ -40,6 +41,10 @@
 //              Scales are powers of two, so those tiles are exact and everything
 //              behind them is the same for all formats.
 //
+// P is rounded to bf16: the product takes both operands in one type, and V is kept in
+// bf16.  That is off by at most 2^-8 of sum p |v|, as in the block-sparse kernel; the sum
+// of a row's weights takes them unrounded.
+//
 // What nobody sees.  A masked logit is replaced, not added to, so K may hold
 // anything.  V meets P = 0 in the product, where NaN and infinity would not
 // stay away: on steps that some row of the item does not see whole (`partial`),
@@ -50,9 +55,10 @@
 //
 // Every wait is bounded (common.cuh).
 //
-// Measured: 1560 tokens over 18720 keys of 12 heads, bf16, 219 us (817 TFLOP/s) and
-// over 32760 keys of 40 heads, e4m3, 1400-1460 us (715-745 TFLOP/s); 1536 tokens over
-// 132000 keys, bf16, 960-985 TFLOP/s.  A step of 128 keys of two tiles takes about 4300
+// Measured (cold caches / the same call again): 1560 tokens over 18720 keys of 12 heads,
+// bf16, 234 / 220 us (768 / 814 TFLOP/s), e4m3 297 / 284, int8 287 / 275; over 32760 keys
+// of 40 heads e4m3 1400 / 1392 us (747 / 752), int8 1389 / 1378; 1536 tokens over 132000
+// keys of 12 heads, bf16, 1294 us (962).  A step of 128 keys of two tiles takes about 4300
 // cycles (tensor pipe 43 % busy, exponentials 41 %), bound by the chain S -> softmax ->
 // P V of each tile; e4m3 about 5500, its unpacking sharing issue slots and ALU with the
 // softmax.
@@ -70,8 +76,10 @@ constexpr int kCacheMaxCtas = 148;      // CTAs of a split launch, one for each 
 // step takes 0.57 of a wide one in bf16, 0.62 in 8 bits, 0.48 at D = 64; counted alike,
 // 1560 tokens over 18720 keys took 234 us instead of 220.
 constexpr int kWideUnits = 5, kNarrowUnits = 3;
-// An item's start and end, in the launch's longest steps (1 / 2 / 3 / 4: 230 / 216 / 204 /
-// 206 us for eight ragged sequences at D = 128, 184 / 175 / 177 / 182 at D = 64).
+// An item's start and end, in the launch's longest steps.  Tiles (1 / 2 / 3 / 4): 230 / 216 /
+// 204 / 206 us for eight ragged sequences at D = 128, 184 / 175 / 177 / 182 at D = 64.
+// Single tokens (1 / 2 / 3 / 5): 64 sequences of up to 4000 keys, 32 heads on 8, int8 94 /
+// 88 / 84 / 84 us, e4m3 94 / 88 / 86 / 88, bf16 117 / 119 / 119 / 119; long caches within 2 %.
 constexpr int kCacheItemCost = 3;
 constexpr int kCacheLeastRun = 3;       // what a CTA takes at least, in those steps
 constexpr int kSegRing = 4;
@@ -769,7 +777,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, FMT, QT>::kThreads, 1)
         p.part_desc[2 * blockIdx.x] = p.part_desc[2 * blockIdx.x + 1] = make_int4(0, 0, kPartNone, 0);
     } else {
       head = blockIdx.y;
-      place = p.slots - 1 - static_cast<int>(blockIdx.x);   // later tokens see more: longest first
+      place = p.slots - 1 - static_cast<int>(blockIdx.x);   // a sequence's later tokens see more: they first
       left = 1;
     }
     if (lane == 0) {

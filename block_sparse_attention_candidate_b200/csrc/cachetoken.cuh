@@ -35,9 +35,12 @@
 // a segment they are joined in shared memory while the SM's other CTAs read on.  An SM
 // runs twelve warps: two CTAs of six, or three of four (8-bit, NT = 1).
 //
-// Measured on 8 K / V heads of D 128 (times of the launch and its join):
-//   3 x 131072 keys, 64 heads: e4m3 166 us (5.0 TB/s), int8 152 (5.5), bf16 243-252 (6.4-6.6);
-//   64 sequences of up to 16000 keys, 32 heads: int8 184 us (5.3), bf16 295 (6.4).
+// Measured on 8 K / V heads of D 128 (the launch and its join, cold caches / the same call
+// again):
+//   3 x 131072 keys, 64 heads: e4m3 183 / 167 us (4.6 / 5.0 TB/s), int8 174 / 155 (4.8 / 5.4),
+//     bf16 262 / 242 (6.1 / 6.6);
+//   64 sequences of up to 16000 keys, 32 heads: int8 203 / 187 us (4.8 / 5.3), e4m3 215 / 202
+//     (4.6 / 4.9), bf16 334 / 289 (5.7 / 6.6).
 // 8-bit pages are bound by issue (unpacking a byte and scaling it), not by HBM.  Pairs
 // of blocks share the softmax step's shuffles and votes: with single blocks and eight
 // warps in each of three CTAs (80 registers) the 8-bit times were 182, 170 and 212 us;

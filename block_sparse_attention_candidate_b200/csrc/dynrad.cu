@@ -1262,6 +1262,10 @@ int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, i
   // sequences of 131,072 keys in e4m3 333 / 168, in bf16 252 / 252; a ragged batch of 64
   // up to 16,000 keys in int8 486 / 189, in bf16 383 / 294; one token over 777 keys in
   // bf16 18.9 / 10.9 on the GPU.  Beyond 16 rows its products would repeat the unpacking.
+  // The average decides for the whole call, so a long chunk among single tokens goes with
+  // them and reads its history 16 rows at a time, or takes them with it: 63 tokens over
+  // 4000 keys each and a chunk over 32760 (12 heads), of 961 tokens 1339 us in bf16 and
+  // 1700-1890 in e4m3, of 1024 (all by tiles) 514 and 653; in two calls 252 + 240 and 178 + 281.
   pl->token_tiles = 0;
   for (int nt = 2; nt >= 1; --nt)
     if (pl->group <= 8 * nt &&
@@ -1279,7 +1283,13 @@ int cache_plan(const dynrad_kv_cache* c, int32_t num_seqs, int32_t num_tokens, i
   // The even cut pays while items are few or single sequences may be most of the
   // work.  Full items in many waves leave little to even out, and keep a head's
   // keys in L2 when they run head after head; with few keys an item is done before
-  // the parts could be joined.
+  // the parts could be joined.  "Full" goes by rows and "many" by places: with 5 to 16
+  // query heads to a K / V head of the single tokens' kernel an item may be one token, so
+  // that batches of 1184 / (2 * K / V heads) sequences on are not cut either.  That is even
+  // where their lengths are (64 heads on 8, 73 cut / 74 not, 2000 keys each: bf16 123 / 117
+  // us, e4m3 94 / 96, int8 88 / 100) and slow where one is far longer, which one CTA
+  // then walks (one of 131072 keys: bf16 199 / 1135, e4m3 148 / 2659, int8 141 / 2394;
+  // 32 heads on 8, cut at 74 too: 199, 148, 137).
   const bool many = slots * c->heads >= 8 * kCacheMaxCtas &&
                     static_cast<int64_t>(num_tokens) >= static_cast<int64_t>(num_seqs) * pl->item_tokens;
   pl->split = slots <= kCacheMaxPlan && !many &&

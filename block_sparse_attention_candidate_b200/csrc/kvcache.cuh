@@ -221,7 +221,10 @@ constexpr int kCacheThreads = 256;
 // over 32,760 tokens of 40 heads (write e4m3 / write bf16 / read e4m3, us): heads
 // inside 216 / 252 / 212; tokens inside, 32 tokens 189 / 268 / 212, 16 tokens 183 /
 // 228 / 189, 8 tokens 183 / 216 / 171; with four units' loads in flight (here) 173 /
-// 220 / 169, which is 5.9-6.1 TB/s.
+// 220 / 169, which is 5.9-6.1 TB/s.  Few heads leave threads without a unit and the time
+// to the look-ups of 4,096 CTAs (32,760 tokens at D = 128, write bf16 / write e4m3 / read
+// e4m3): 8 heads 49 / 45 / 43 us (5.5 / 4.5 / 4.7 TB/s), 5 heads 35 / 37 / 33, 2 heads 23 /
+// 29 / 25, one head 18 / 25 / 20 (1.8 / 1.0 / 1.2 TB/s).
 constexpr int kCacheTokens = 8;
 constexpr int kCacheCtasPerSm = 4;
 constexpr int kCacheUnroll = 4;    // units whose loads a thread has in flight

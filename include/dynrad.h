@@ -575,13 +575,15 @@ int dynrad_cache_read(const dynrad_kv_cache *cache, const dynrad_seqs *seqs,
  *                 with another or with one of q; o may lie between q's rows
  *                 (two slices of one tensor) with the same strides only
  *   heads         query heads, a multiple of cache->heads, at most 128 to each
- *   scale         logit scale, a normal number; 0 means 1/sqrt(dim)
+ *   scale         logit scale, a positive normal number; 0 means 1/sqrt(dim)
  *   lse           DEVICE fp32 [heads, num_tokens], apart from q and o
  *   workspace     DEVICE, 256-byte aligned, at least
  *                 dynrad_cache_attn_workspace_bytes(...) bytes (0 if it can not
  *                 be sized), apart from the other operands; its contents do not
  *                 matter and none are kept.
  *                 Calls that overlap on the GPU need a workspace each.
+ * One kernel serves a whole call, by its average of tokens a sequence: a long chunk
+ * beside many single tokens is faster in a call of its own.
  * Errors: DYNRAD_ERR_INVALID_ARG / UNSUPPORTED / CAPACITY before any launch.
  */
 size_t dynrad_cache_attn_workspace_bytes(const dynrad_kv_cache *cache,
