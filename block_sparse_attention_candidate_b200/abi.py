@@ -675,8 +675,8 @@ def dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens=None, head_m
     """(K, V) that the cache holds at the tokens' positions, bf16 [T, heads, D]
     or, head_major, [heads, T, D] (with one sequence the tensors that
     dynrad_select_blocks and dynrad_sparse_attn take, but for the batch axis).
-    T = num_tokens, or that of the tensors in ``out``; rows behind
-    cu_seq[-1] are left as they are."""
+    T = num_tokens, or that of the tensors in ``out``, which must not overlap; rows
+    behind cu_seq[-1] are left as they are."""
     if stream is not None:    # what is allocated here belongs to that stream too
         with torch.cuda.stream(stream):
             return dynrad_cache_read(cache, page_table, cu_seq, kv_len, num_tokens, head_major, out)
